@@ -10,9 +10,7 @@
 
 #include "ep_internal.h"
 
-namespace {
-
-using namespace ep;
+namespace ep {
 
 ep_status_t check_shape(const ep_shape_t *s) {
     if (s == nullptr) return EP_ERR_INVALID_ARG;
@@ -28,6 +26,12 @@ ep_status_t check_shape(const ep_shape_t *s) {
     if ((int64_t)s->num_tokens * s->num_ranks > INT_MAX) return EP_ERR_UNSUPPORTED;
     return EP_OK;
 }
+
+}  // namespace ep
+
+namespace {
+
+using namespace ep;
 
 bool aligned16(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
 

@@ -73,6 +73,9 @@ inline Workspace workspace_layout(int64_t T, int R, int E, int C, int K) {
     return w;
 }
 
+// The host checks of ep_shape_t that every call makes first.
+ep_status_t check_shape(const ep_shape_t *s);
+
 // ---------------------------------------------------------------- launchers
 hipError_t launch_layout(const ep_shape_t &s, const int64_t *topk_idx, int32_t *per_rank, int32_t *per_node,
                          int32_t *per_expert, uint8_t *in_rank, char *ws, int32_t *dev_status, hipStream_t stream);

@@ -1,0 +1,285 @@
+"""The router and its gradient against their definitions in binary64."""
+import itertools
+
+import numpy as np
+import pytest
+import torch
+
+import experts_oracle as oracle64
+from combine_ep_get_02_amd import ep, experts
+
+pytestmark = pytest.mark.gpu
+KINDS = {"sigmoid": experts.EP_SCORE_SIGMOID, "softmax": experts.EP_SCORE_SOFTMAX}
+U = oracle64.U
+
+
+def _logits(rng, T, E, dtype):
+    """Values as the type holds them, and the tensor."""
+    t = torch.from_numpy((rng.standard_normal((T, E)) * 1.5).astype(np.float32)).to(dtype)
+    return t.to(torch.float32).numpy(), t.cuda()
+
+
+def _route(logits, bias, kind, k, groups=1, kept=1, best=1, renorm=True, scale=1.0, mask=None, ranks=1):
+    T, E = logits.shape
+    shape = ep.make_shape(T, 8, k, E, ranks, 1)
+    r = experts.make_router(KINDS[kind], groups, kept, best, renorm, scale)
+    idx = torch.full((T + 1, k), -777, dtype=torch.int64, device="cuda")
+    w = torch.full((T + 1, k), -3.0, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    experts.ep_route(shape, r, logits, bias, mask, idx[:T], w[:T], status)
+    torch.cuda.synchronize()
+    assert bool((idx[T] == -777).all()) and bool((w[T] == -3.0).all())
+    return idx[:T].cpu().numpy(), w[:T].cpu().numpy(), int(status.item())
+
+
+def _weights_near(got, want, kind, renorm):
+    # numerators and their sum are formed in 64 bits and rounded once (a step is 2 U, half of it U).
+    # A softmax that is not renormalised also divides by a sum of E 32-bit exponentials: an
+    # exponential of d <= 0 is off by (|d| + 4) U, the terms' weights average |d| + 4 to under 16
+    # here, and a tree over up to 2048 terms (32 in a lane, 6 steps across) adds at most 38 U.
+    tol = 2 * U if kind == "sigmoid" or renorm else 56 * U
+    assert np.all(np.abs(got - want) <= tol * np.abs(want) + 1e-44)
+
+
+@pytest.mark.parametrize("E", [1, 2, 5, 16, 60, 64, 65, 128, 160, 256, 384, 1000, 2048])
+@pytest.mark.parametrize("kind,dtype,renorm", [("sigmoid", torch.float32, True), ("softmax", torch.bfloat16, False),
+                                               ("softmax", torch.float32, True)])
+def test_choice_and_weights(E, kind, dtype, renorm):
+    rng = np.random.default_rng(E)
+    k = min(8, E)
+    for T, with_bias in ((1, False), (37, True), (130, False)):
+        print(f"[route] E={E} {kind} {dtype} T={T} bias={with_bias}", flush=True)
+        values, logits = _logits(rng, T, E, dtype)
+        bias = (rng.standard_normal(E) * 0.1).astype(np.float32) if with_bias else None
+        got_i, got_w, status = _route(logits, None if bias is None else torch.from_numpy(bias).cuda(), kind, k,
+                                      renorm=renorm, scale=1.0 if renorm else 2.5)
+        want_i, want_w = oracle64.route(values, bias, kind, k, 1, 1, 1, renorm, 1.0 if renorm else 2.5)
+        assert np.array_equal(got_i, want_i)
+        _weights_near(got_w, want_w, kind, renorm)
+        assert status == 0
+
+
+@pytest.mark.parametrize("E,groups,kept", [(256, 8, 4), (64, 64, 9), (160, 8, 3), (12, 4, 4), (96, 2, 1), (1024, 16, 1)])
+@pytest.mark.parametrize("best", [1, 2])
+@pytest.mark.parametrize("kind", sorted(KINDS))
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_groups(E, groups, kept, best, kind, with_bias):
+    rng = np.random.default_rng(E + best)
+    print(f"[route] groups E={E} G={groups} kept={kept} best={best} {kind} bias={with_bias}", flush=True)
+    values, logits = _logits(rng, 70, E, torch.float32)
+    bias = (rng.standard_normal(E) * 0.1).astype(np.float32) if with_bias else None
+    k = 8  # more than the groups kept hold, in some cases: the rest of the slots stay empty
+    got_i, got_w, _ = _route(logits, None if bias is None else torch.from_numpy(bias).cuda(), kind, k, groups, kept,
+                             best, True, 2.5)
+    want_i, want_w = oracle64.route(values, bias, kind, k, groups, kept, best, True, 2.5)
+    assert np.array_equal(got_i, want_i)
+    _weights_near(got_w, want_w, kind, True)
+
+
+@pytest.mark.parametrize("kind", sorted(KINDS))
+@pytest.mark.parametrize("with_bias", [False, True])
+def test_ties_go_to_the_lowest_expert(kind, with_bias):
+    """Few distinct values: nearly every choice and every group rating is a tie."""
+    rng = np.random.default_rng(3)
+    values = rng.integers(-2, 3, size=(200, 64)).astype(np.float32)
+    bias = (rng.integers(0, 2, size=64) * 0.25).astype(np.float32) if with_bias else None
+    dbias = None if bias is None else torch.from_numpy(bias).cuda()
+    for dtype, (groups, kept, best) in itertools.product((torch.float32, torch.bfloat16), ((1, 1, 1), (8, 3, 2), (8, 3, 1))):
+        got_i, got_w, _ = _route(torch.from_numpy(values).to(dtype).cuda(), dbias, kind, 6, groups, kept, best)
+        want_i, want_w = oracle64.route(values, bias, kind, 6, groups, kept, best, True, 1.0)
+        assert np.array_equal(got_i, want_i)
+        _weights_near(got_w, want_w, kind, True)
+
+
+@pytest.mark.parametrize("kind", sorted(KINDS))
+def test_near_ties_are_decided_as_in_64_bits(kind):
+    """Choices that differ by less than a step of f32, and logits so large that scores saturate."""
+    rng = np.random.default_rng(11)
+    T, E = 64, 256
+    values = np.repeat(rng.standard_normal((T, 1)), E, 1).astype(np.float32)
+    values = np.nextafter(values, np.where(rng.random((T, E)) < 0.5, 9, -9).astype(np.float32)).astype(np.float32)
+    bias = np.zeros(E, np.float32)
+    bias[rng.integers(0, E, 20)] = np.float32(1e-9)
+    logits = torch.from_numpy(values).cuda()
+    for b in (None, bias):
+        got_i, got_w, _ = _route(logits, None if b is None else torch.from_numpy(b).cuda(), kind, 8, 8, 4, 2)
+        want_i, want_w = oracle64.route(values, b, kind, 8, 8, 4, 2, True, 1.0)
+        assert np.array_equal(got_i, want_i)
+        _weights_near(got_w, want_w, kind, True)
+    big = (30 + 60 * rng.random((T, E))).astype(np.float32)
+    for v in (big, -big):
+        got_i, _, _ = _route(torch.from_numpy(v).cuda(), None, kind, 8)
+        assert np.array_equal(got_i, oracle64.route(v, None, kind, 8, 1, 1, 1, True, 1.0)[0])
+
+
+@pytest.mark.parametrize("kind", sorted(KINDS))
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("groups", [1, 4])
+def test_masked_experts_tokens_and_bad_values(kind, renorm, groups):
+    rng = np.random.default_rng(5)
+    T, E, k = 24, 32, 6
+    values = (rng.standard_normal((T, E)) * 1.5).astype(np.float32)
+    values[0] = -np.inf                                   # nothing to choose
+    values[1, 3:] = -np.inf                               # three experts for six slots
+    values[2, :] = np.finfo(np.float32).min               # the type's lowest value is a value
+    values[3, ::2] = np.finfo(np.float32).min
+    values[4, 0], values[4, 1] = np.nan, np.inf
+    values[5] = np.nan
+    values[6, 5] = np.finfo(np.float32).max
+    values[7] = -800.0                                    # every sigmoid is 0 in 64 bits: no sum to divide by
+    values[8, 0] = -np.nan
+    bias = (rng.standard_normal(E) * 0.1).astype(np.float32)
+    bias[7] = -np.inf
+    mask = np.ones(T, np.uint8)
+    mask[20:] = 0
+    for b in (None, bias):
+        got_i, got_w, status = _route(torch.from_numpy(values).cuda(), None if b is None else torch.from_numpy(b).cuda(),
+                                      kind, k, groups, max(1, groups - 2), 2 if groups > 1 else 1, renorm, 1.0,
+                                      torch.from_numpy(mask).cuda())
+        want_i, want_w = oracle64.route(values, b, kind, k, groups, max(1, groups - 2), 2 if groups > 1 else 1, renorm,
+                                        1.0, mask)
+        assert np.array_equal(got_i, want_i)
+        assert np.all(np.isfinite(got_w))
+        _weights_near(got_w, want_w, kind, renorm)
+        assert status == experts.EP_DEV_BAD_LOGIT
+    # rows switched off are not read: their bad values are not flagged
+    values[:20] = 0.0
+    values[20:] = np.nan
+    _, _, status = _route(torch.from_numpy(values).cuda(), None, kind, k, mask=torch.from_numpy(mask).cuda())
+    assert status == 0
+    bias[3] = np.nan
+    got_i, _, status = _route(torch.from_numpy(values[:20]).cuda(), torch.from_numpy(bias).cuda(), kind, k)
+    assert status == experts.EP_DEV_BAD_LOGIT and not np.isin(got_i, (3, 7)).any()
+
+
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_rows_apart(dtype):
+    """Logits and their gradient as columns of wider tensors, at offsets that break 16-byte alignment."""
+    rng = np.random.default_rng(7)
+    T, E, k = 50, 60, 4
+    values, _ = _logits(rng, T, E, dtype)
+    for lead, extra in ((0, 0), (1, 0), (3, 7), (4, 4)):
+        wide = torch.full((T, lead + E + extra), float("nan"), dtype=dtype, device="cuda")
+        view = wide[:, lead:lead + E]
+        view.copy_(torch.from_numpy(values))
+        got_i, got_w, status = _route(view, None, "sigmoid", k)
+        want_i, want_w = oracle64.route(values, None, "sigmoid", k, 1, 1, 1, True, 1.0)
+        assert np.array_equal(got_i, want_i) and status == 0
+        _weights_near(got_w, want_w, "sigmoid", True)
+        out = torch.full_like(wide, 7.0)
+        gw = rng.standard_normal((T, k)).astype(np.float32)
+        shape = ep.make_shape(T, 8, k, E, 1, 1)
+        experts.ep_route_backward(shape, experts.make_router(1), view, torch.from_numpy(got_i).cuda(),
+                                  torch.from_numpy(gw).cuda(), out[:, lead:lead + E])
+        assert bool((out[:, :lead] == 7.0).all()) and bool((out[:, lead + E:] == 7.0).all())
+        _check_gradient(out[:, lead:lead + E], values, got_i, gw, "sigmoid", True, 1.0)
+
+
+def _check_gradient(got, values, idx, gw, kind, renorm, scale):
+    want, size, before = oracle64.route_backward(values, idx, gw, kind, renorm, scale)
+    # sigmoid: two 32-bit sigmoids of at most 8 U each (an exponential, a sum, a quotient), the slots'
+    # sum and two products: under 24 U of `size`.  Softmax: a score of at most 56 U (as for the
+    # weights, with its own exponential) times a difference off by 3 U of `size`.
+    # Renormalising takes g_j - sum g_i s_i / S in binary64, where up to k + 6 steps of 2^-53 each
+    # leave up to 40 * 2^-53 of what is subtracted even where the difference is 0 (one slot alone).
+    tol = (24 if kind == "sigmoid" else 64) * U * size + 40 * 2.0 ** -53 * before
+    if got.dtype == torch.bfloat16:
+        tol = tol + oracle64.BF16_HALF * np.abs(want)
+    err = np.abs(got.double().cpu().numpy() - want)
+    assert np.all(err <= tol + 1e-37), float((err - tol).max())
+
+
+@pytest.mark.parametrize("E", [1, 7, 64, 160, 256, 2048])
+@pytest.mark.parametrize("kind", sorted(KINDS))
+@pytest.mark.parametrize("renorm", [False, True])
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+def test_gradient_against_the_formula(E, kind, renorm, dtype):
+    rng = np.random.default_rng(E + 1)
+    T, k = 33, min(8, E)
+    print(f"[route] gradient E={E} {kind} renorm={renorm} {dtype}", flush=True)
+    values, logits = _logits(rng, T, E, dtype)
+    idx = np.stack([rng.choice(E, k, replace=False) for _ in range(T)]).astype(np.int64)
+    idx[0] = -1
+    idx[1, 0] = -1
+    idx[2, :] = idx[2, 0]  # one expert in every slot
+    gw = rng.standard_normal((T, k)).astype(np.float32)
+    gw[3] = 0.0
+    out = torch.full((T, E), float("nan"), dtype=dtype, device="cuda")
+    status = torch.zeros(1, dtype=torch.int32, device="cuda")
+    experts.ep_route_backward(ep.make_shape(T, 8, k, E, 1, 1), experts.make_router(KINDS[kind], 1, 1, 1, renorm, 2.5), logits,
+                              torch.from_numpy(idx).cuda(), torch.from_numpy(gw).cuda(), out, status)
+    assert int(status.item()) == 0
+    assert not out[0].any() and not out[3].any()
+    _check_gradient(out, values, idx, gw, kind, renorm, 2.5)
+
+
+@pytest.mark.parametrize("kind", sorted(KINDS))
+@pytest.mark.parametrize("renorm", [False, True])
+def test_gradient_against_differences(kind, renorm):
+    """Central differences of the weights in binary64, the choice held fixed."""
+    rng = np.random.default_rng(2)
+    T, E, k = 6, 24, 4
+    values, logits = _logits(rng, T, E, torch.float32)
+    idx, _ = oracle64.route(values, None, kind, k, 1, 1, 1, renorm, 1.5)
+    gw = rng.standard_normal((T, k)).astype(np.float32)
+
+    def value(v):
+        p = np.take_along_axis(oracle64.scores(v, kind), idx, 1)
+        w = 1.5 * (p / p.sum(1, keepdims=True) if renorm else p)
+        return (w * gw).sum()
+
+    h = 1e-5
+    want = np.zeros((T, E))
+    for t, e in itertools.product(range(T), range(E)):
+        up, down = values.astype(np.float64), values.astype(np.float64)
+        up[t, e] += h
+        down[t, e] -= h
+        want[t, e] = (value(up) - value(down)) / (2 * h)
+    out = torch.empty(T, E, device="cuda")
+    experts.ep_route_backward(ep.make_shape(T, 8, k, E, 1, 1), experts.make_router(KINDS[kind], 1, 1, 1, renorm, 1.5), logits,
+                              torch.from_numpy(idx).cuda(), torch.from_numpy(gw).cuda(), out)
+    # truncation h^2 times a third derivative below 10, rounding 2^-53 * 20 / h, and 64 U of values below 4
+    assert np.allclose(out.cpu().numpy(), want, rtol=0, atol=2e-5)
+
+
+def test_gradient_of_masked_and_bad_logits():
+    T, E, k = 4, 8, 3
+    values = np.random.default_rng(1).standard_normal((T, E)).astype(np.float32)
+    values[0, :4] = -np.inf
+    values[1] = -np.inf
+    values[2, 0] = np.finfo(np.float32).min
+    idx = np.array([[5, 6, -1], [0, 1, 2], [0, 1, 2], [1, 99, -5]], np.int64)
+    gw = np.ones((T, k), np.float32)
+    gw[:, 1] = -2.0
+    for kind, renorm in itertools.product(sorted(KINDS), (False, True)):
+        out = torch.full((T, E), float("nan"), device="cuda")
+        status = torch.zeros(1, dtype=torch.int32, device="cuda")
+        experts.ep_route_backward(ep.make_shape(T, 8, k, E, 1, 1), experts.make_router(KINDS[kind], 1, 1, 1, renorm),
+                                  torch.from_numpy(values).cuda(), torch.from_numpy(idx).cuda(),
+                                  torch.from_numpy(gw).cuda(), out, status)
+        assert int(status.item()) == ep.EP_DEV_BAD_TOPK_IDX
+        _check_gradient(out, values, idx, gw, kind, renorm, 1.0)
+        bad = values.copy()
+        bad[3, 7] = np.nan
+        status.zero_()
+        experts.ep_route_backward(ep.make_shape(T, 8, k, E, 1, 1), experts.make_router(KINDS[kind], 1, 1, 1, renorm),
+                                  torch.from_numpy(bad).cuda(), torch.from_numpy(idx).cuda(),
+                                  torch.from_numpy(gw).cuda(), out, status)
+        assert int(status.item()) == ep.EP_DEV_BAD_TOPK_IDX | experts.EP_DEV_BAD_LOGIT
+        _check_gradient(out, bad, idx, gw, kind, renorm, 1.0)
+
+
+def test_no_tokens_and_many_slots():
+    empty = torch.empty(0, 16, device="cuda")
+    idx, w, status = _route(empty, None, "sigmoid", 4)
+    assert idx.shape == (0, 4) and status == 0
+    rng = np.random.default_rng(4)
+    values, logits = _logits(rng, 9, 40, torch.float32)
+    got_i, got_w, _ = _route(logits, None, "softmax", 32)
+    want_i, want_w = oracle64.route(values, None, "softmax", 32, 1, 1, 1, True, 1.0)
+    assert np.array_equal(got_i, want_i)
+    _weights_near(got_w, want_w, "softmax", True)
+    values, logits = _logits(rng, 9, 5, torch.float32)
+    got_i, _, _ = _route(logits, None, "softmax", 32)
+    assert np.array_equal(got_i, oracle64.route(values, None, "softmax", 32, 1, 1, 1, True, 1.0)[0])
+    assert np.all(got_i[:, 5:] == -1)
