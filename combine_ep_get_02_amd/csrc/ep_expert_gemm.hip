@@ -1,12 +1,21 @@
 // ep_expert_gemm.hip -- the experts' products on the grouped rows: E4M3 codes with a scale for each
 // block of 128 on matrix cores (gfx950).  Definitions in ep_experts.h.
 //
-// out[m][c] = sum over blocks b of sx[m][b] sw[c / 128][b] * (x[m] . w[c] over block b).  One
-// v_mfma_f32_16x16x128_f8f6f4 covers exactly one block of 128 channels, so each takes a zero
-// accumulator and its 16 x 16 result is scaled into the f32 sums by ordinary fused multiply-adds
-// (the instruction's own scales are powers of two and cannot hold these).  The weights are the A
-// operand and the rows the B operand, so a lane's four results are four neighbouring columns of one
-// row: one scale a lane and contiguous stores.
+// out[m][c] = sum over blocks b of sx[m][b] sw[c / 128][b] * (x[m] . w[c] over block b).  Each block
+// of 128 channels starts from a zero accumulator, and its result is scaled into the f32 sums by
+// ordinary fused multiply-adds (the matrix instructions' own scales are powers of two and cannot
+// hold these).  The weights are the A operand and the rows the B operand, so a lane's results are
+// neighbouring columns of one row: one scale a lane and contiguous stores.
+//
+// Two kinds of matrix instruction serve:
+//   - bf16 outputs take the E4M3 instructions, at twice the f16 rate.  They add the eight products of
+//     a group of neighbouring channels with 13 bits below the largest one's, the rest of a product
+//     being cut (measured: 2^8 keeps 2^-5 of its group and loses 2^-6), and the groups in f32.
+//     Against f32 that is 1.5e-5 of the result for normally distributed codes, a hundredth of the
+//     rounding to bf16 that follows.
+//   - the SwiGLU form's scales leave in f32, where 1.5e-5 would show.  It takes the f16 instructions
+//     on codes turned into f16 (exact: every E4M3 value is one, and a product of two fits f32), whose
+//     sums are f32 throughout (measured 1e-8).
 #include <limits.h>
 
 #include "ep_experts_internal.h"
@@ -17,6 +26,7 @@ namespace {
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
+typedef float f32x16 __attribute__((ext_vector_type(16)));
 
 // What a block works on: rows [first, first + rows) of the grouped rows, all of expert `expert`.
 struct Tile {
@@ -66,151 +76,450 @@ __device__ __forceinline__ Tile find_tile(const GemmArgs &p, int bm, int index, 
     return t;
 }
 
-constexpr int kBM = 128, kBN = 256, kThreads = 256;
 constexpr int kUnits = kScaleBlock / 16;  // 16-byte units of a row in one block of channels
+constexpr int kBlockThreads = 512;
 
-// LDS place of unit c of row r: rotating the units by the row spreads the 16 rows that a wave reads
-// at once over all banks.
-__device__ __forceinline__ int place(int r, int c) { return r * kUnits + (c ^ (r & (kUnits - 1))); }
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
 
-// kBM rows x kBN weight rows a block, 2 x 2 waves of 64 x 128.  SWIGLU: each wave's 128 weight rows
-// are 64 gate rows and the 64 up rows of the same outputs.
-template <bool SWIGLU>
-__global__ __launch_bounds__(kThreads) void expert_gemm_kernel(GemmArgs p, int col_tiles) {
-    __shared__ u32x4 s_x[kBM * kUnits];
-    __shared__ u32x4 s_w[kBN * kUnits];
-    __shared__ float s_top[2][kBM];
-    const int lane = threadIdx.x & (kWave - 1), wave = threadIdx.x >> 6;
-    const int wm = wave >> 1, wn = wave & 1;
+// Half of a 16-byte unit of codes (which: 0 or 1) as one f16 operand of a 32 x 32 x 16 product.
+// Every E4M3 value is an f16 value.
+template <int which>
+__device__ __forceinline__ f16x8 to_f16(u32x4 unit) {
+    f16x8 f;
+#pragma unroll
+    for (int i = 0; i < 2; ++i) {
+        const int word = (int)unit[2 * which + i];
+        const f16x2 a = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word, 1.0f, false);
+        const f16x2 b = __builtin_amdgcn_cvt_scalef32_pk_f16_fp8(word, 1.0f, true);
+        f[4 * i] = a[0];
+        f[4 * i + 1] = a[1];
+        f[4 * i + 2] = b[0];
+        f[4 * i + 3] = b[1];
+    }
+    return f;
+}
+
+// Two units of codes as one operand of a matrix instruction on codes.
+__device__ __forceinline__ i32x8 codes(u32x4 lo, u32x4 hi) {
+    return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
+}
+
+// Buffer descriptor over `bytes` bytes from p; loads past them return 0.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t descriptor(const void *p, uint32_t bytes) {
+    return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)bytes, 0x00027000);
+}
+
+// 64 lanes' 16-byte units from global memory straight into 1 KiB of LDS at dst (wave-uniform).
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t src, u32x4 *dst, int voffset, int soffset) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void *)dst, 16, voffset, soffset,
+                                             0, 0);
+}
+
+// The same for 4-byte values: 256 bytes of LDS.
+__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t src, float *dst, int voffset, int soffset) {
+    __builtin_amdgcn_raw_ptr_buffer_load_lds(src, (__attribute__((address_space(3))) void *)dst, 4, voffset, soffset,
+                                             0, 0);
+}
+
+// Ends a step: the wave's loads into LDS have landed and its reads are over, and then every wave's.
+__device__ __forceinline__ void end_step() {
+    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
+    __syncthreads();
+}
+
+// Unit of row r that lies at place c of its row in LDS (and the place of unit c).  A 16-byte read
+// is served 16 lanes at a time, lanes whose rows share their low three bits among them; so bits 3
+// and 4 take part.
+__device__ __forceinline__ int rotate(int r, int c) { return c ^ ((r ^ ((r >> 3) & 3)) & (kUnits - 1)); }
+
+constexpr int kBN = 256;  // weight rows of a wide block
+
+// 2 x 4 waves of 32 MI rows x 64 weight rows.
+template <bool SWIGLU, int MI>
+__global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(GemmArgs p, int col_tiles) {
+    constexpr int WM = 2, WN = 4, BM = 32 * MI * WM, HALF = 32;
+    static_assert(2 * HALF * WN == kBN, "256 weight rows a block");
+    constexpr int XL = BM * kUnits / kBlockThreads, WL = kBN * kUnits / kBlockThreads;  // units a thread loads
+    // Two buffers: while one block of channels is multiplied the next is on its way.  A wave's last
+    // load of a step is of scales: rows' by the first BM lanes, the weights' two by the lanes of the
+    // next wave (the others repeat those).  (One array a buffer: the compiler tells them apart, and
+    // would wait for all loads before a read of an array that it does not.)
+    static_assert(BM <= 64 * (WM * WN - 1), "a wave is left for the weights' scales");
+    constexpr int kX = 0, kW = BM * kUnits, kS = kW + kBN * kUnits, kBuffer = kS + kBlockThreads / 4;
+    __shared__ u32x4 s_0[kBuffer], s_1[kBuffer];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int wm = wave / WN, wn = wave % WN;
     const int col_tile = blockIdx.x % col_tiles;
-    const Tile t = find_tile(p, kBM, blockIdx.x / col_tiles, blockIdx.x == 0);
+    const Tile t = find_tile(p, BM, blockIdx.x / col_tiles, blockIdx.x == 0);
     if (t.rows == 0) return;  // the whole block: every wave found the same
-    const int wrows = SWIGLU ? 2 * p.n : p.n;  // weight rows of an expert
+    const int wrows = SWIGLU ? 2 * p.n : p.n;
     const int blocks = p.k / kScaleBlock;
     const int scale_rows = (wrows + kScaleBlock - 1) / kScaleBlock;
-    const uint8_t *x = p.x + t.first * p.k;
-    const uint8_t *w = p.w + (int64_t)t.expert * wrows * p.k;
-    const float *sx = p.x_scales + t.first * blocks;
-    const float *sw = p.w_scales + (int64_t)t.expert * scale_rows * blocks;
+    const __amdgpu_buffer_rsrc_t xbuf = descriptor(p.x + t.first * p.k, (uint32_t)t.rows * p.k);
+    const __amdgpu_buffer_rsrc_t wbuf = descriptor(p.w + (int64_t)t.expert * wrows * p.k, (uint32_t)wrows * p.k);
 
-    // weight row behind row v of the block's kBN
-    auto weight_row = [&](int v) {
-        if constexpr (SWIGLU) {
-            const int u = v & 127, c = col_tile * 128 + (v >> 7) * 64 + (u & 63);
-            return u < 64 ? c : p.n + c;
-        } else {
-            const int c = col_tile * kBN + v;
-            return c < p.n ? c : p.n - 1;  // a column past the last is computed and not stored
-        }
-    };
-    int scale_row0, scale_row1;  // of the wave's first and second 64 weight rows
+    // where the lane's first unit of a buffer comes from; the others lie kStep rows on, each.  Units
+    // go to LDS in lane order, so the rotation of a row's units is in the address they are read
+    // from.  Rows past the segment, or past the last column, are past the descriptor's end: they
+    // read as 0 and are not stored.
+    constexpr int kStep = kBlockThreads / kUnits;
+    const int r0 = threadIdx.x / kUnits, c0 = rotate(r0, threadIdx.x & (kUnits - 1)) * 16;
+    static_assert(kStep % 32 == 0, "a step keeps a row's rotation");
+    const int x_first = r0 * p.k + c0;
+    int w_first;
+    if constexpr (SWIGLU) {
+        // half of a wave's weight rows are gate rows, half the up rows of the same outputs
+        static_assert(kStep % (2 * HALF) == 0, "a step keeps a row's place in its half");
+        const int c = col_tile * 128 + r0 / (2 * HALF) * HALF + r0 % HALF;
+        w_first = ((r0 & HALF) ? p.n + c : c) * p.k + c0;
+    } else {
+        w_first = (col_tile * kBN + r0) * p.k + c0;
+    }
+    int scale_row0, scale_row1;  // of the first and the second 128 weight rows; gate and up
     if constexpr (SWIGLU) {
         scale_row0 = col_tile;
         scale_row1 = p.n / kScaleBlock + col_tile;
     } else {
-        scale_row0 = col_tile * (kBN / kScaleBlock) + wn;
-        scale_row0 = scale_row1 = scale_row0 < scale_rows ? scale_row0 : scale_rows - 1;
+        scale_row0 = 2 * col_tile;
+        scale_row1 = 2 * col_tile + 1 < scale_rows ? 2 * col_tile + 1 : scale_rows - 1;
+    }
+    const __amdgpu_buffer_rsrc_t sbuf =
+        wave * kWave < BM ? descriptor(p.x_scales + t.first * blocks, (uint32_t)t.rows * blocks * 4)
+                          : descriptor(p.w_scales + (int64_t)t.expert * scale_rows * blocks, (uint32_t)scale_rows * blocks * 4);
+    const int sat = (wave * kWave < BM ? (int)threadIdx.x : (lane & 1) ? scale_row1 : scale_row0) * blocks * 4;
+
+    f32x16 acc[MI][2];
+#pragma unroll
+    for (int i = 0; i < MI; ++i)
+#pragma unroll
+        for (int j = 0; j < 2; ++j)
+#pragma unroll
+            for (int e = 0; e < 16; ++e) acc[i][j][e] = 0.0f;
+
+    const int half = lane >> 5, r32 = lane & 31;
+    const bool busy = wm * 32 * MI < t.rows;  // the other half of a part tile has nothing to multiply
+    auto load = [&](u32x4 *to, int b) {
+        int xat = x_first, wat = w_first;
+        asm volatile("" : "+v"(xat), "+v"(wat));  // as in multiply()
+#pragma unroll
+        for (int i = 0; i < XL; ++i)
+            load_to_lds(xbuf, to + kX + i * kBlockThreads + wave * kWave, xat + i * kStep * p.k, b * kScaleBlock);
+#pragma unroll
+        for (int i = 0; i < WL; ++i)
+            load_to_lds(wbuf, to + kW + i * kBlockThreads + wave * kWave, wat + i * (SWIGLU ? kStep / 2 : kStep) * p.k,
+                        b * kScaleBlock);
+        load_to_lds(sbuf, reinterpret_cast<float *>(to + kS) + wave * kWave, sat, b * 4);
+    };
+    auto multiply = [&](const u32x4 *from) {
+        const u32x4 *x = from + kX, *w = from + kW;
+        const float *s = reinterpret_cast<const float *>(from + kS);
+        // the lane's units of any row it reads: 2 u + half, where the rotation has put them
+        int u0 = rotate(r32, half);
+        asm volatile("" : "+v"(u0));  // addresses are cheaper formed anew than kept in registers
+        auto unit_of = [&](const u32x4 *rows, int r, int u) { return rows[r * kUnits + (u0 ^ (2 * u))]; };
+        f16x8 fw[2][8];  // SWIGLU: the wave's weights as f16
+        i32x8 cw[2][2];  // otherwise: their codes
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const u32x4 unit = unit_of(w, wn * 64 + j * 32 + r32, u);
+                if constexpr (SWIGLU) {
+                    fw[j][2 * u] = to_f16<0>(unit);
+                    fw[j][2 * u + 1] = to_f16<1>(unit);
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) cw[j][u >> 1][(u & 1) * 4 + k] = (int)unit[k];
+                }
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const int r = wm * 32 * MI + i * 32 + r32;
+            f32x16 part[2];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) part[0][e] = part[1][e] = 0.0f;
+            if constexpr (SWIGLU) {
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const u32x4 unit = unit_of(x, r, u);
+                    const f16x8 a = to_f16<0>(unit), b = to_f16<1>(unit);
+                    part[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fw[0][2 * u], a, part[0], 0, 0, 0);
+                    part[1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fw[1][2 * u], a, part[1], 0, 0, 0);
+                    part[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fw[0][2 * u + 1], b, part[0], 0, 0, 0);
+                    part[1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fw[1][2 * u + 1], b, part[1], 0, 0, 0);
+                }
+            } else {
+                i32x8 cx[2];
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const u32x4 unit = unit_of(x, r, u);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) cx[u >> 1][(u & 1) * 4 + k] = (int)unit[k];
+                }
+#pragma unroll
+                for (int j = 0; j < 2; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        part[j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(cw[j][h], cx[h], part[j], 0, 0, 0, 0, 0, 0);
+            }
+            const float scale[2] = {s[r] * s[BM + (SWIGLU ? 0 : wn >> 1)], s[r] * s[BM + (SWIGLU ? 1 : wn >> 1)]};
+#pragma unroll
+            for (int j = 0; j < 2; ++j)
+#pragma unroll
+                for (int e = 0; e < 16; ++e) acc[i][j][e] = __builtin_fmaf(part[j][e], scale[j], acc[i][j][e]);
+            if constexpr (!SWIGLU) __builtin_amdgcn_sched_barrier(0);  // 3 % against free order
+        }
+    };
+    // one block of channels: start the next one's loads and multiply
+    auto step = [&](const u32x4 *now, u32x4 *next, int b) {
+        if (b + 1 < blocks) load(next, b + 1);
+        if (busy) multiply(now);
+        end_step();
+    };
+    load(s_0, 0);
+    end_step();
+    for (int b = 0; b < blocks; b += 2) {
+        step(s_0, s_1, b);
+        if (b + 1 < blocks) step(s_1, s_0, b + 1);
     }
 
-    constexpr int MT = 4, NT = 8;
-    f32x4 acc[MT][NT];
+    // the lane's element e of a 32 x 32 result: row r32, weight row 8 (e / 4) + 4 half + e % 4
+    if constexpr (!SWIGLU) {
+        uint16_t *out = static_cast<uint16_t *>(p.out);
 #pragma unroll
-    for (int i = 0; i < MT; ++i)
+        for (int i = 0; i < MI; ++i) {
+            const int r = wm * 32 * MI + i * 32 + r32;
+            if (r >= t.rows) continue;
 #pragma unroll
-        for (int j = 0; j < NT; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+            for (int j = 0; j < 2; ++j) {
+#pragma unroll
+                for (int g = 0; g < 4; ++g) {
+                    const int c = col_tile * kBN + wn * 64 + j * 32 + g * 8 + half * 4;
+                    if (c >= p.n) continue;  // n is a multiple of 8: all four or none
+                    uint2 o;
+                    o.x = pack_bf16(acc[i][j][4 * g], acc[i][j][4 * g + 1]);
+                    o.y = pack_bf16(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]);
+                    *reinterpret_cast<uint2 *>(out + (t.first + r) * p.n + c) = o;
+                }
+            }
+        }
+    } else {
+        float *s_top = reinterpret_cast<float *>(s_0);  // [WN][BM]: the tiles are done with
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            float top = 0.0f;
+#pragma unroll
+            for (int e = 0; e < 16; ++e) {
+                const float g = acc[i][0][e], u = acc[i][1][e];
+                const float a = g / (1.0f + expf(-g)) * u;
+                acc[i][0][e] = a;
+                top = fmaxf(top, fabsf(a));
+            }
+            top = fmaxf(top, __shfl_xor(top, 32));
+            if (half == 0) s_top[wn * BM + wm * 32 * MI + i * 32 + r32] = top;
+        }
+        __syncthreads();
+        uint8_t *out = static_cast<uint8_t *>(p.out);
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            const int r = wm * 32 * MI + i * 32 + r32;
+            if (r >= t.rows) continue;
+            float m = kE4m3AmaxFloor;
+#pragma unroll
+            for (int j = 0; j < WN; ++j) m = fmaxf(m, s_top[j * BM + r]);
+            const float inv = kE4m3Max / m;
+            if (wn == 0 && half == 0) p.out_scales[(t.first + r) * (p.n / kScaleBlock) + col_tile] = m / kE4m3Max;
+#pragma unroll
+            for (int g = 0; g < 4; ++g) {
+                const int c = col_tile * 128 + wn * HALF + g * 8 + half * 4;
+                *reinterpret_cast<uint32_t *>(out + (t.first + r) * p.n + c) =
+                    e4m3_pack4(acc[i][0][4 * g] * inv, acc[i][0][4 * g + 1] * inv, acc[i][0][4 * g + 2] * inv,
+                               acc[i][0][4 * g + 3] * inv);
+            }
+        }
+    }
+}
+
+// Few rows: 16 MF rows x 64 NG weight rows a block of NG x KS waves.  The weights are read once and
+// by one wave only, so they go straight to registers: no LDS, no barrier, and every wave has the
+// next block of channels on its way while it multiplies one.  The KS waves of a group take every
+// KS-th block of channels and add up through LDS at the end.
+template <bool SWIGLU, int MF, int NG, int KS, int WAVES>
+__global__ __launch_bounds__(NG *KS *kWave, WAVES) void expert_gemm_narrow_kernel(GemmArgs p, int col_tiles) {
+    static_assert(!SWIGLU || NG == 4, "a block holds a scale's 128 outputs");
+    constexpr int BM = 16 * MF, BN = 64 * NG;
+    constexpr int OWN = (SWIGLU ? 2 : 4) / KS;  // 16-column results of its group that a wave finishes
+    __shared__ f32x4 s_sum[NG][KS][4][MF][kWave];
+    __shared__ float s_top[NG * KS][BM];
+    const int lane = threadIdx.x & (kWave - 1);
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    const int group = wave % NG, ks = wave / NG;
+    const int col_tile = blockIdx.x % col_tiles;
+    const Tile t = find_tile(p, BM, blockIdx.x / col_tiles, blockIdx.x == 0);
+    if (t.rows == 0) return;  // the whole block: every wave found the same
+    const int wrows = SWIGLU ? 2 * p.n : p.n;
+    const int blocks = p.k / kScaleBlock;
+    const int scale_rows = (wrows + kScaleBlock - 1) / kScaleBlock;
+    const __amdgpu_buffer_rsrc_t xbuf = descriptor(p.x + t.first * p.k, (uint32_t)t.rows * p.k);
+    const __amdgpu_buffer_rsrc_t wbuf = descriptor(p.w + (int64_t)t.expert * wrows * p.k, (uint32_t)wrows * p.k);
+    const __amdgpu_buffer_rsrc_t sbuf = descriptor(p.x_scales + t.first * blocks, (uint32_t)t.rows * blocks * 4);
 
     const int q = lane >> 4, r16 = lane & 15;
-    for (int b = 0; b < blocks; ++b) {
-        __syncthreads();
-        for (int i = threadIdx.x; i < kBM * kUnits; i += kThreads) {
-            const int r = i / kUnits, c = i % kUnits;
-            const int row = r < t.rows ? r : t.rows - 1;  // rows past the segment are not stored
-            s_x[place(r, c)] = *reinterpret_cast<const u32x4 *>(x + (int64_t)row * p.k + b * kScaleBlock + c * 16);
-        }
-        for (int i = threadIdx.x; i < kBN * kUnits; i += kThreads) {
-            const int r = i / kUnits, c = i % kUnits;
-            s_w[place(r, c)] =
-                *reinterpret_cast<const u32x4 *>(w + (int64_t)weight_row(r) * p.k + b * kScaleBlock + c * 16);
-        }
-        __syncthreads();
-        const float sw0 = sw[(int64_t)scale_row0 * blocks + b], sw1 = sw[(int64_t)scale_row1 * blocks + b];
-        auto fragment = [&](const u32x4 *s, int r) {
-            const u32x4 lo = s[place(r, 2 * q)], hi = s[place(r, 2 * q + 1)];
-            return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-        };
-        i32x8 fx[MT];
-        float scale[MT];
+    // column (output) of the group's first weight row; SWIGLU: rows 0-31 are gate rows, 32-63 the up rows of the same
+    const int c0 = SWIGLU ? col_tile * 128 + group * 32 : col_tile * BN + group * 64;
+    int wat[4];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int r = wm * 64 + i * 16 + r16;
-            fx[i] = fragment(s_x, r);
-            scale[i] = sx[(int64_t)(r < t.rows ? r : t.rows - 1) * blocks + b];
+    for (int j = 0; j < 4; ++j) {
+        const int row = SWIGLU ? (j < 2 ? c0 + j * 16 : p.n + c0 + (j - 2) * 16) : c0 + j * 16;
+        wat[j] = (row + r16) * p.k + q * 16;  // rows past the last are past the descriptor's end and read as 0
+    }
+    const float *sw0 = p.w_scales + (int64_t)t.expert * scale_rows * blocks;
+    const float *sw1;
+    if constexpr (SWIGLU) {
+        sw1 = sw0 + (int64_t)(p.n / kScaleBlock + col_tile) * blocks;
+        sw0 += (int64_t)col_tile * blocks;
+    } else {
+        sw0 += (int64_t)(c0 / kScaleBlock < scale_rows ? c0 / kScaleBlock : scale_rows - 1) * blocks;
+        sw1 = sw0;
+    }
+
+    struct Codes {
+        u32x4 w[4][2], x[MF][2];
+        float sx[MF], sw[2];
+    };
+    auto load = [&](Codes &c, int b) {
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            c.w[j][0] = __builtin_amdgcn_raw_buffer_load_b128(wbuf, wat[j], b * kScaleBlock, 0);
+            c.w[j][1] = __builtin_amdgcn_raw_buffer_load_b128(wbuf, wat[j] + 64, b * kScaleBlock, 0);
         }
 #pragma unroll
-        for (int j = 0; j < NT; ++j) {
-            const i32x8 fw = fragment(s_w, wn * 128 + j * 16 + r16);
-            const float swj = j < NT / 2 ? sw0 : sw1;
+        for (int i = 0; i < MF; ++i) {
+            const int at = (i * 16 + r16) * p.k + q * 16;
+            c.x[i][0] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, at, b * kScaleBlock, 0);
+            c.x[i][1] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, at + 64, b * kScaleBlock, 0);
+            c.sx[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sbuf, (i * 16 + r16) * blocks * 4, b * 4, 0));
+        }
+        c.sw[0] = sw0[b];
+        c.sw[1] = SWIGLU ? sw1[b] : c.sw[0];
+    };
+    f32x4 acc[MF][4];
 #pragma unroll
-            for (int i = 0; i < MT; ++i) {
-                const f32x4 part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                    fw, fx[i], f32x4{0.f, 0.f, 0.f, 0.f}, 0, 0, 0, 0, 0, 0);
-                const float s = scale[i] * swj;
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    auto multiply = [&](const Codes &c) {
+        f16x8 fx[MF][4];
+        if constexpr (SWIGLU) {
+#pragma unroll
+            for (int i = 0; i < MF; ++i)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    fx[i][2 * h] = to_f16<0>(c.x[i][h]);
+                    fx[i][2 * h + 1] = to_f16<1>(c.x[i][h]);
+                }
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            f16x8 fw[4];
+            if constexpr (SWIGLU) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    fw[2 * h] = to_f16<0>(c.w[j][h]);
+                    fw[2 * h + 1] = to_f16<1>(c.w[j][h]);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < MF; ++i) {
+                f32x4 part = {0.f, 0.f, 0.f, 0.f};
+                if constexpr (SWIGLU) {
+#pragma unroll
+                    for (int k = 0; k < 4; ++k)
+                        part = __builtin_amdgcn_mfma_f32_16x16x32_f16(fw[k], fx[i][k], part, 0, 0, 0);
+                } else {
+                    part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(codes(c.w[j][0], c.w[j][1]),
+                                                                            codes(c.x[i][0], c.x[i][1]), part, 0, 0, 0,
+                                                                            0, 0, 0);
+                }
+                const float s = c.sx[i] * c.sw[j >> 1];
 #pragma unroll
                 for (int k = 0; k < 4; ++k) acc[i][j][k] = __builtin_fmaf(part[k], s, acc[i][j][k]);
             }
         }
+    };
+    Codes even, odd;
+    if (ks < blocks) load(even, ks);
+    for (int b = ks; b < blocks; b += 2 * KS) {
+        if (b + KS < blocks) load(odd, b + KS);
+        multiply(even);
+        if (b + 2 * KS < blocks) load(even, b + 2 * KS);
+        if (b + KS < blocks) multiply(odd);
     }
 
+    // the KS sums of each 16 x 16 result, added in order by the wave that finishes it
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+#pragma unroll
+        for (int i = 0; i < MF; ++i) s_sum[group][ks][j][i][lane] = acc[i][j];
+    __syncthreads();
+    auto total = [&](int j, int i) {
+        f32x4 v = s_sum[group][0][j][i][lane];
+#pragma unroll
+        for (int k = 1; k < KS; ++k) v += s_sum[group][k][j][i][lane];
+        return v;
+    };
     if constexpr (!SWIGLU) {
-        uint32_t *out = static_cast<uint32_t *>(p.out);
+        uint16_t *out = static_cast<uint16_t *>(p.out);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int r = wm * 64 + i * 16 + r16;
-            if (r >= t.rows) continue;
+        for (int i = 0; i < MF; ++i) {
+            const int r = i * 16 + r16;
 #pragma unroll
-            for (int j = 0; j < NT; ++j) {
-                const int c = col_tile * kBN + wn * 128 + j * 16 + q * 4;
-                if (c >= p.n) continue;  // n is a multiple of 8: all four or none
-                uint2 o;
-                o.x = pack_bf16(acc[i][j][0], acc[i][j][1]);
-                o.y = pack_bf16(acc[i][j][2], acc[i][j][3]);
-                *reinterpret_cast<uint2 *>(out + ((t.first + r) * p.n + c) / 2) = o;
+            for (int o = 0; o < OWN; ++o) {
+                const int j = ks * OWN + o, c = c0 + j * 16 + q * 4;
+                const f32x4 v = total(j, i);
+                if (r >= t.rows || c >= p.n) continue;  // n is a multiple of 8: all four or none
+                uint2 pair;
+                pair.x = pack_bf16(v[0], v[1]);
+                pair.y = pack_bf16(v[2], v[3]);
+                *reinterpret_cast<uint2 *>(out + (t.first + r) * p.n + c) = pair;
             }
         }
     } else {
-        float top[MT];
+        f32x4 a[MF][OWN];
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            top[i] = 0.0f;
+        for (int i = 0; i < MF; ++i) {
+            float top = 0.0f;
 #pragma unroll
-            for (int j = 0; j < NT / 2; ++j) {
+            for (int o = 0; o < OWN; ++o) {
+                const f32x4 g = total(ks * OWN + o, i), u = total(2 + ks * OWN + o, i);
 #pragma unroll
                 for (int k = 0; k < 4; ++k) {
-                    const float g = acc[i][j][k], u = acc[i][j + NT / 2][k];
-                    const float a = g / (1.0f + expf(-g)) * u;
-                    acc[i][j][k] = a;
-                    top[i] = fmaxf(top[i], fabsf(a));
+                    a[i][o][k] = g[k] / (1.0f + expf(-g[k])) * u[k];
+                    top = fmaxf(top, fabsf(a[i][o][k]));
                 }
             }
-            top[i] = fmaxf(top[i], __shfl_xor(top[i], 16));
-            top[i] = fmaxf(top[i], __shfl_xor(top[i], 32));
-            if (q == 0) s_top[wn][wm * 64 + i * 16 + r16] = top[i];
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            if (q == 0) s_top[wave][i * 16 + r16] = top;
         }
         __syncthreads();
-        uint32_t *out = static_cast<uint32_t *>(p.out);
+        uint8_t *out = static_cast<uint8_t *>(p.out);
 #pragma unroll
-        for (int i = 0; i < MT; ++i) {
-            const int r = wm * 64 + i * 16 + r16;
+        for (int i = 0; i < MF; ++i) {
+            const int r = i * 16 + r16;
             if (r >= t.rows) continue;
-            const float m = fmaxf(fmaxf(s_top[0][r], s_top[1][r]), kE4m3AmaxFloor);
-            const float inv = kE4m3Max / m;
-            if (wn == 0 && q == 0) p.out_scales[(t.first + r) * (p.n / kScaleBlock) + col_tile] = m / kE4m3Max;
+            float m = kE4m3AmaxFloor;
 #pragma unroll
-            for (int j = 0; j < NT / 2; ++j) {
-                const int c = col_tile * 128 + wn * 64 + j * 16 + q * 4;
-                out[((t.first + r) * p.n + c) / 4] = e4m3_pack4(acc[i][j][0] * inv, acc[i][j][1] * inv,
-                                                               acc[i][j][2] * inv, acc[i][j][3] * inv);
-            }
+            for (int j = 0; j < NG * KS; ++j) m = fmaxf(m, s_top[j][r]);
+            const float inv = kE4m3Max / m;
+            if (wave == 0 && q == 0) p.out_scales[(t.first + r) * (p.n / kScaleBlock) + col_tile] = m / kE4m3Max;
+#pragma unroll
+            for (int o = 0; o < OWN; ++o)
+                *reinterpret_cast<uint32_t *>(out + (t.first + r) * p.n + c0 + (ks * OWN + o) * 16 + q * 4) =
+                    e4m3_pack4(a[i][o][0] * inv, a[i][o][1] * inv, a[i][o][2] * inv, a[i][o][3] * inv);
         }
     }
 }
@@ -221,25 +530,45 @@ int64_t row_tiles(const GemmArgs &a, int bm) {
     return a.num_rows / bm + busy;  // each segment ends in at most one part tile
 }
 
-int64_t grid_blocks(const GemmArgs &a) {
-    const int64_t cols = a.swiglu ? a.n / kScaleBlock : (a.n + kBN - 1) / kBN;
-    return row_tiles(a, kBM) * cols;
+// A kernel for a product, and what a block of it works on.
+struct Plan {
+    void (*kernel)(GemmArgs, int);
+    int threads, rows, cols;
+};
+
+template <bool SWIGLU, int MF, int NG, int KS, int WAVES>
+Plan narrow() {
+    return {expert_gemm_narrow_kernel<SWIGLU, MF, NG, KS, WAVES>, NG * KS * kWave, 16 * MF, SWIGLU ? 128 : 64 * NG};
+}
+
+Plan plan(const GemmArgs &a) {
+    const int mean = a.num_rows / a.num_experts;
+    if (a.swiglu) {
+        if (mean <= 8) return narrow<true, 1, 4, 1, 3>();
+        if (mean <= 32) return narrow<true, 2, 4, 1, 2>();
+        return {expert_gemm_wide_kernel<true, 2>, kBlockThreads, 128, 128};
+    }
+    if (mean <= 8) return narrow<false, 1, 2, 2, 3>();
+    if (mean <= 32) return narrow<false, 2, 2, 2, 2>();
+    return {expert_gemm_wide_kernel<false, 4>, kBlockThreads, 256, kBN};
+}
+
+int64_t grid_blocks(const GemmArgs &a, const Plan &pl) {
+    return row_tiles(a, pl.rows) * ((a.n + pl.cols - 1) / pl.cols);
 }
 
 }  // namespace
 
-bool gemm_grid_ok(const GemmArgs &a) { return grid_blocks(a) <= INT_MAX / kThreads; }
+bool gemm_grid_ok(const GemmArgs &a) {
+    const Plan pl = plan(a);
+    return grid_blocks(a, pl) <= INT_MAX / pl.threads;
+}
 
 hipError_t launch_expert_gemm(const GemmArgs &a, hipStream_t stream) {
-    const int64_t blocks = grid_blocks(a);
+    const Plan pl = plan(a);
+    const int64_t blocks = grid_blocks(a, pl);
     if (blocks == 0) return hipSuccess;
-    if (a.swiglu) {
-        hipLaunchKernelGGL(expert_gemm_kernel<true>, dim3((unsigned)blocks), dim3(kThreads), 0, stream, a,
-                           a.n / kScaleBlock);
-    } else {
-        hipLaunchKernelGGL(expert_gemm_kernel<false>, dim3((unsigned)blocks), dim3(kThreads), 0, stream, a,
-                           (a.n + kBN - 1) / kBN);
-    }
+    hipLaunchKernelGGL(pl.kernel, dim3((unsigned)blocks), dim3(pl.threads), 0, stream, a, (a.n + pl.cols - 1) / pl.cols);
     return hipGetLastError();
 }
 

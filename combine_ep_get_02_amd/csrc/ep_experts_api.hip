@@ -32,7 +32,8 @@ ep_status_t gemm_checked(const GemmArgs &a) {
         return EP_ERR_INVALID_ARG;
     if (a.swiglu && a.n % kScaleBlock != 0) return EP_ERR_INVALID_ARG;
     if (a.expert_rows == nullptr && a.num_experts != 1) return EP_ERR_INVALID_ARG;
-    if ((int64_t)a.n * (a.swiglu ? 2 : 1) * a.k > INT_MAX || a.num_experts > kMaxGemmExperts) return EP_ERR_UNSUPPORTED;
+    if ((int64_t)a.n * (a.swiglu ? 2 : 1) * a.k > INT_MAX || a.k > kMaxGemmK || a.num_experts > kMaxGemmExperts)
+        return EP_ERR_UNSUPPORTED;
     if (!gemm_grid_ok(a)) return EP_ERR_UNSUPPORTED;
     if (a.num_rows == 0) return EP_OK;
     if (a.x == nullptr || a.x_scales == nullptr || a.w == nullptr || a.w_scales == nullptr || a.out == nullptr ||

@@ -10,6 +10,7 @@ namespace ep {
 constexpr int kMaxRouteExperts = 2048;
 constexpr int kMaxRouteGroups = 64;  // one group per lane of a wave
 constexpr int kMaxGemmExperts = 16384;
+constexpr int kMaxGemmK = 1 << 20;  // a tile's rows are within reach of a 32-bit offset
 constexpr int kScaleBlock = 128;  // channels (and weight rows) per scale
 
 struct RouteArgs {

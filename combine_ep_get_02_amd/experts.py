@@ -14,7 +14,7 @@ from dataclasses import dataclass
 import torch
 
 from combine_ep_get_02_amd import ep
-from combine_ep_get_02_amd.ep import _check, _ptr, _stream
+from combine_ep_get_02_amd.ep import _check, _stream
 
 EP_DEV_BAD_LOGIT = 32
 EP_LOGITS_F32, EP_LOGITS_BF16 = 0, 1
@@ -57,39 +57,49 @@ def load() -> ctypes.CDLL:
 
 
 _ONE_BYTE = (torch.uint8, torch.float8_e4m3fn)
+_BF16, _F32, _I32, _I64 = (torch.bfloat16,), (torch.float32,), (torch.int32,), (torch.int64,)
+_MASK = (torch.uint8, torch.bool)
 _LOGITS = {torch.float32: EP_LOGITS_F32, torch.bfloat16: EP_LOGITS_BF16}
 
 
-def _need(name, t, count, dtype, optional=False) -> None:
-    """`t` holds at least `count` elements of `dtype` on the current device, without gaps."""
-    if t is None:
-        if optional or count <= 0:
-            return
-        raise ValueError(f"{name}: missing")
-    if t.dtype not in (dtype if isinstance(dtype, tuple) else (dtype,)):
-        raise ValueError(f"{name}: {t.dtype}, not {dtype}")
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, not on the current GPU")
-    if not t.is_contiguous():
-        raise ValueError(f"{name}: not contiguous")
-    if t.numel() < count:
-        raise ValueError(f"{name}: {t.numel()} elements, {count} needed")
+def _device() -> int:
+    """The current GPU; none before the first use of one, when no tensor can be on it."""
+    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
 
 
-def _status_word(dev_status) -> None:
-    _need("dev_status", dev_status, 1, torch.int32, optional=True)
+def _raw_stream(stream, device) -> int | None:
+    # the handle alone: building torch's stream object costs as much as the rest of a small call
+    if stream is None and device >= 0:
+        return torch._C._cuda_getCurrentRawStream(device)
+    return _stream(stream)
 
 
-def _logit_rows(name, t, tokens, experts, dtype=None) -> int:
+def _at(name, t, count, dtypes, device) -> int | None:
+    """Address of a tensor of at least `count` elements of one of `dtypes` on `device`, without gaps."""
+    if t is None and count <= 0:
+        return None
+    if t is None or t.get_device() != device or t.dtype not in dtypes or not t.is_contiguous() or t.numel() < count:
+        _refuse(name, t, f"{count} contiguous elements of {dtypes}")
+    return t.data_ptr()
+
+
+def _at_or_null(name, t, count, dtypes, device) -> int | None:
+    return None if t is None else _at(name, t, count, dtypes, device)
+
+
+def _refuse(name, t, wanted) -> None:
+    got = "None" if t is None else f"{tuple(t.shape)} {t.dtype} strides {t.stride()} on {t.device}"
+    raise ValueError(f"{name}: {got}, but {wanted} on the current GPU needed")
+
+
+def _logit_rows(name, t, tokens, experts, device, dtype=None) -> int:
     """The stride between rows of a [tokens][experts] tensor whose rows may lie apart."""
-    if t.dim() != 2 or t.shape[0] < tokens or t.shape[1] < experts or t.dtype not in _LOGITS or \
-            (dtype is not None and t.dtype != dtype):
-        raise ValueError(f"{name}: {tuple(t.shape)} {t.dtype}, not [{tokens}][{experts}] float32 or bfloat16")
-    if t.device.type != "cuda" or t.device.index != torch.cuda.current_device():
-        raise ValueError(f"{name}: on {t.device}, not on the current GPU")
-    if (t.shape[1] > 1 and t.stride(1) != 1) or (t.shape[0] > 1 and t.stride(0) < experts):
-        raise ValueError(f"{name}: strides {t.stride()}")
-    return max(t.stride(0), experts)
+    rows, columns = t.shape if t.dim() == 2 else (-1, -1)
+    apart, along = t.stride() if t.dim() == 2 else (0, 0)
+    if t.get_device() != device or t.dtype not in _LOGITS or (dtype is not None and t.dtype != dtype) or \
+            rows < tokens or columns < experts or (columns > 1 and along != 1) or (rows > 1 and apart < experts):
+        _refuse(name, t, f"[{tokens}][{experts}] of {dtype or 'float32 or bfloat16'}, rows without gaps,")
+    return max(apart, experts)
 
 
 def make_router(score, num_groups=1, groups_kept=1, group_best=1, renormalize=True, weight_scale=1.0) -> ep_router_t:
@@ -97,97 +107,86 @@ def make_router(score, num_groups=1, groups_kept=1, group_best=1, renormalize=Tr
 
 
 def ep_route(shape, router, logits, bias, token_mask, topk_idx, topk_weights, dev_status=None, stream=None) -> None:
-    T, K = shape.num_tokens, shape.num_topk
-    stride = _logit_rows("logits", logits, T, shape.num_experts)
-    _need("bias", bias, shape.num_experts, torch.float32, optional=True)
-    _need("token_mask", token_mask, T, (torch.uint8, torch.bool), optional=True)
-    _need("topk_idx", topk_idx, T * K, torch.int64)
-    _need("topk_weights", topk_weights, T * K, torch.float32)
-    _status_word(dev_status)
-    _check(load().ep_route(ctypes.byref(shape), ctypes.byref(router), _ptr(logits), _LOGITS[logits.dtype], stride,
-                           _ptr(bias), _ptr(token_mask), _ptr(topk_idx), _ptr(topk_weights), _ptr(dev_status),
-                           _stream(stream)), "ep_route")
+    T, K, E, at = shape.num_tokens, shape.num_topk, shape.num_experts, _device()
+    stride = _logit_rows("logits", logits, T, E, at)
+    _check(load().ep_route(
+        ctypes.byref(shape), ctypes.byref(router), logits.data_ptr(), _LOGITS[logits.dtype], stride,
+        _at_or_null("bias", bias, E, _F32, at), _at_or_null("token_mask", token_mask, T, _MASK, at),
+        _at("topk_idx", topk_idx, T * K, _I64, at), _at("topk_weights", topk_weights, T * K, _F32, at),
+        _at_or_null("dev_status", dev_status, 1, _I32, at), _raw_stream(stream, at)), "ep_route")
 
 
 def ep_route_backward(shape, router, logits, topk_idx, grad_weights, grad_logits, dev_status=None,
                       stream=None) -> None:
-    T, K = shape.num_tokens, shape.num_topk
-    stride = _logit_rows("logits", logits, T, shape.num_experts)
-    grad_stride = _logit_rows("grad_logits", grad_logits, T, shape.num_experts, logits.dtype)
-    _need("topk_idx", topk_idx, T * K, torch.int64)
-    _need("grad_weights", grad_weights, T * K, torch.float32)
-    _status_word(dev_status)
-    _check(load().ep_route_backward(ctypes.byref(shape), ctypes.byref(router), _ptr(logits), _LOGITS[logits.dtype],
-                                    stride, _ptr(topk_idx), _ptr(grad_weights), _ptr(grad_logits), grad_stride,
-                                    _ptr(dev_status), _stream(stream)), "ep_route_backward")
+    T, K, E, at = shape.num_tokens, shape.num_topk, shape.num_experts, _device()
+    stride = _logit_rows("logits", logits, T, E, at)
+    grad_stride = _logit_rows("grad_logits", grad_logits, T, E, at, logits.dtype)
+    _check(load().ep_route_backward(
+        ctypes.byref(shape), ctypes.byref(router), logits.data_ptr(), _LOGITS[logits.dtype], stride,
+        _at("topk_idx", topk_idx, T * K, _I64, at), _at("grad_weights", grad_weights, T * K, _F32, at),
+        grad_logits.data_ptr(), grad_stride, _at_or_null("dev_status", dev_status, 1, _I32, at),
+        _raw_stream(stream, at)), "ep_route_backward")
 
 
-def _need_product(num_experts, weight_rows, k, x, x_scales, w, w_scales, expert_rows, num_rows) -> None:
+def _product_arguments(num_experts, n, weight_rows, k, x, x_scales, w, w_scales, expert_rows, num_rows, at):
     blocks = k // SCALE_BLOCK
-    _need("x", x, num_rows * k, _ONE_BYTE)
-    _need("x_scales", x_scales, num_rows * blocks, torch.float32)
-    _need("w", w, num_experts * weight_rows * k, _ONE_BYTE)
-    _need("w_scales", w_scales, num_experts * -(-weight_rows // SCALE_BLOCK) * blocks, torch.float32)
-    _need("expert_rows", expert_rows, num_experts, torch.int32, optional=True)
+    return (num_experts, n, k, _at("x", x, num_rows * k, _ONE_BYTE, at),
+            _at("x_scales", x_scales, num_rows * blocks, _F32, at),
+            _at("w", w, num_experts * weight_rows * k, _ONE_BYTE, at),
+            _at("w_scales", w_scales, num_experts * -(-weight_rows // SCALE_BLOCK) * blocks, _F32, at),
+            _at_or_null("expert_rows", expert_rows, num_experts, _I32, at), num_rows)
 
 
 def ep_expert_gemm_fp8(num_experts, n, k, x, x_scales, w, w_scales, expert_rows, num_rows, out, dev_status=None,
                        stream=None) -> None:
-    _need_product(num_experts, n, k, x, x_scales, w, w_scales, expert_rows, num_rows)
-    _need("out", out, num_rows * n, torch.bfloat16)
-    _status_word(dev_status)
-    _check(load().ep_expert_gemm_fp8(int(num_experts), int(n), int(k), _ptr(x), _ptr(x_scales), _ptr(w),
-                                     _ptr(w_scales), _ptr(expert_rows), int(num_rows), _ptr(out), _ptr(dev_status),
-                                     _stream(stream)), "ep_expert_gemm_fp8")
+    at = _device()
+    _check(load().ep_expert_gemm_fp8(
+        *_product_arguments(num_experts, n, n, k, x, x_scales, w, w_scales, expert_rows, num_rows, at),
+        _at("out", out, num_rows * n, _BF16, at), _at_or_null("dev_status", dev_status, 1, _I32, at),
+        _raw_stream(stream, at)), "ep_expert_gemm_fp8")
 
 
 def ep_expert_gemm_swiglu_fp8(num_experts, n, k, x, x_scales, w, w_scales, expert_rows, num_rows, out, out_scales,
                               dev_status=None, stream=None) -> None:
-    _need_product(num_experts, 2 * n, k, x, x_scales, w, w_scales, expert_rows, num_rows)
-    _need("out", out, num_rows * n, _ONE_BYTE)
-    _need("out_scales", out_scales, num_rows * (n // SCALE_BLOCK), torch.float32)
-    _status_word(dev_status)
-    _check(load().ep_expert_gemm_swiglu_fp8(int(num_experts), int(n), int(k), _ptr(x), _ptr(x_scales), _ptr(w),
-                                            _ptr(w_scales), _ptr(expert_rows), int(num_rows), _ptr(out),
-                                            _ptr(out_scales), _ptr(dev_status), _stream(stream)),
-           "ep_expert_gemm_swiglu_fp8")
+    at = _device()
+    _check(load().ep_expert_gemm_swiglu_fp8(
+        *_product_arguments(num_experts, n, 2 * n, k, x, x_scales, w, w_scales, expert_rows, num_rows, at),
+        _at("out", out, num_rows * n, _ONE_BYTE, at),
+        _at("out_scales", out_scales, num_rows * (n // SCALE_BLOCK), _F32, at),
+        _at_or_null("dev_status", dev_status, 1, _I32, at), _raw_stream(stream, at)), "ep_expert_gemm_swiglu_fp8")
 
 
-def _need_combine(shape, y, topk_idx, topk_weights, send_slot, slot_pos, num_recv_rows, num_grouped_rows) -> None:
+def _combine_arguments(shape, y, topk_idx, topk_weights, send_slot, slot_pos, num_recv_rows, num_grouped_rows, at):
     T, K = shape.num_tokens, shape.num_topk
-    _need("y", y, num_grouped_rows * shape.hidden if T > 0 else 0, torch.bfloat16)
-    _need("topk_idx", topk_idx, T * K, torch.int64)
-    _need("topk_weights", topk_weights, T * K, torch.float32)
-    _need("send_slot", send_slot, T * shape.num_ranks, torch.int32)
-    _need("slot_pos", slot_pos, num_recv_rows * K, torch.int32)
+    return (_at("y", y, num_grouped_rows * shape.hidden if T > 0 else 0, _BF16, at),
+            _at("topk_idx", topk_idx, T * K, _I64, at), _at("topk_weights", topk_weights, T * K, _F32, at),
+            _at("send_slot", send_slot, T * shape.num_ranks, _I32, at),
+            _at("slot_pos", slot_pos, num_recv_rows * K, _I32, at))
 
 
 def ep_combine_grouped(shape, y, topk_idx, topk_weights, send_slot, slot_pos, num_recv_rows, num_grouped_rows,
                        combined_x, dev_status=None, stream=None) -> None:
-    _need_combine(shape, y, topk_idx, topk_weights, send_slot, slot_pos, num_recv_rows, num_grouped_rows)
-    _need("combined_x", combined_x, shape.num_tokens * shape.hidden, torch.bfloat16)
-    _status_word(dev_status)
-    _check(load().ep_combine_grouped(ctypes.byref(shape), _ptr(y), _ptr(topk_idx), _ptr(topk_weights),
-                                     _ptr(send_slot), _ptr(slot_pos), int(num_recv_rows), int(num_grouped_rows),
-                                     _ptr(combined_x), _ptr(dev_status), _stream(stream)), "ep_combine_grouped")
+    at = _device()
+    _check(load().ep_combine_grouped(
+        ctypes.byref(shape),
+        *_combine_arguments(shape, y, topk_idx, topk_weights, send_slot, slot_pos, num_recv_rows, num_grouped_rows,
+                            at), num_recv_rows, num_grouped_rows,
+        _at("combined_x", combined_x, shape.num_tokens * shape.hidden, _BF16, at),
+        _at_or_null("dev_status", dev_status, 1, _I32, at), _raw_stream(stream, at)), "ep_combine_grouped")
 
 
 def ep_combine_grouped_backward(shape, grad_combined, y, topk_idx, topk_weights, send_slot, slot_pos, grouped_row,
                                 num_grouped, num_recv_rows, num_grouped_rows, grad_y, grad_topk_weights,
                                 dev_status=None, stream=None) -> None:
-    T = shape.num_tokens
-    _need_combine(shape, y, topk_idx, topk_weights, send_slot, slot_pos, num_recv_rows, num_grouped_rows)
-    _need("grad_combined", grad_combined, T * shape.hidden, torch.bfloat16)
-    _need("grouped_row", grouped_row, num_grouped_rows, torch.int32)
-    _need("num_grouped", num_grouped, 1 if num_grouped_rows > 0 else 0, torch.int32)
-    _need("grad_y", grad_y, num_grouped_rows * shape.hidden, torch.bfloat16)
-    _need("grad_topk_weights", grad_topk_weights, T * shape.num_topk, torch.float32)
-    _status_word(dev_status)
-    _check(load().ep_combine_grouped_backward(ctypes.byref(shape), _ptr(grad_combined), _ptr(y), _ptr(topk_idx),
-                                              _ptr(topk_weights), _ptr(send_slot), _ptr(slot_pos), _ptr(grouped_row),
-                                              _ptr(num_grouped), int(num_recv_rows), int(num_grouped_rows),
-                                              _ptr(grad_y), _ptr(grad_topk_weights), _ptr(dev_status),
-                                              _stream(stream)), "ep_combine_grouped_backward")
+    T, H, at = shape.num_tokens, shape.hidden, _device()
+    _check(load().ep_combine_grouped_backward(
+        ctypes.byref(shape), _at("grad_combined", grad_combined, T * H, _BF16, at),
+        *_combine_arguments(shape, y, topk_idx, topk_weights, send_slot, slot_pos, num_recv_rows, num_grouped_rows,
+                            at), _at("grouped_row", grouped_row, num_grouped_rows, _I32, at),
+        _at("num_grouped", num_grouped, 1 if num_grouped_rows > 0 else 0, _I32, at), num_recv_rows,
+        num_grouped_rows, _at("grad_y", grad_y, num_grouped_rows * H, _BF16, at),
+        _at("grad_topk_weights", grad_topk_weights, T * shape.num_topk, _F32, at),
+        _at_or_null("dev_status", dev_status, 1, _I32, at), _raw_stream(stream, at)), "ep_combine_grouped_backward")
 
 
 # ----------------------------------------------------------------------------- an expert layer

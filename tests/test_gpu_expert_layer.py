@@ -94,7 +94,8 @@ def test_layer_against_binary64(shape):
     sizes = layer.b.recv_per_expert.cpu().numpy()
     want_y, mag = oracle64.product(act, act_s.numpy(), layer.w_out, layer.w_out_s, sizes, act.shape[0])
     yv = y.view(torch.bfloat16).double().numpy()
-    tol = oracle64.BF16_HALF * np.abs(want_y) + (2 * (I + I // 128) + 2) * oracle64.U * mag * 1.01
+    cut = oracle64.product_cut(act, act_s.numpy(), layer.w_out, layer.w_out_s, sizes, act.shape[0])
+    tol = oracle64.BF16_HALF * np.abs(want_y) + ((2 * (I + I // 128) + 2) * oracle64.U * mag + 8 * 2.0 ** -13 * cut) * 1.01
     assert np.all(np.abs(yv - want_y) <= tol)
     want, cmag = oracle64.combine(yv, w.numpy(), pos)
     assert np.all(np.abs(got - want) <= oracle64.BF16_HALF * np.abs(want) + 2 * K * oracle64.U * cmag)
