@@ -1,22 +1,31 @@
 // ep_route.hip -- the router: a token's scores, the experts chosen from them and their weights, and
 // the gradient of the weights (gfx950).  Definitions in ep_experts.h.
 //
-// One wave per token.  Lane i holds the VPL consecutive experts from i * VPL, so the lowest lane
-// with the largest value, then the lowest element in it, is the lowest expert: ties need no index.
-// Choices are compared in binary64: a last-bit difference of a 32-bit exp would otherwise decide
-// which of two nearly equal experts a token goes to.
+// A token is 64 lanes or, where there are many tokens and few experts, 16 (four tokens a wave: a
+// round of the selection then costs its cross-lane steps once for four).  Lane i of a token holds
+// the VPL consecutive experts from i * VPL, so the lowest lane with the largest value, then the
+// lowest element in it, is the lowest expert: ties need no index.
+//
+// Choices compare as in binary64 -- a last-bit difference of a 32-bit exp must not decide which of
+// two nearly equal experts a token goes to -- but are formed in f32 first.  With no bias the logits
+// themselves order the experts, and f32 is exact.  Otherwise f32 choices are off by a known part
+// of their size: where two neighbours in the order found, or the last group kept and the best one
+// dropped, are no further apart than that, the wave does the token over in binary64.
+#include <limits.h>
+
 #include "ep_experts_internal.h"
 
 namespace ep {
 namespace {
 
-constexpr int kRouteWaves = 4;  // waves (tokens) per block
+constexpr int kRouteWaves = 4;  // waves per block
+constexpr int64_t kManyTokens = 2048;
 
 struct RouteParams {
     RouteArgs a;
     int64_t T;
     int E, K, G, kept, best, group_size;
-    bool sigmoid, renorm;
+    bool sigmoid, renorm, vector;
     float scale;
 };
 
@@ -24,7 +33,7 @@ struct RouteBackwardParams {
     RouteBackwardArgs a;
     int64_t T;
     int E, K;
-    bool sigmoid, renorm;
+    bool sigmoid, renorm, vector, vector_out;
     float scale;
 };
 
@@ -40,300 +49,681 @@ __device__ __forceinline__ double shfl_xor_f64(double v, int s) {
     return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
-__device__ __forceinline__ double readlane_f64(double v, int src) {
-    return __builtin_bit_cast(double, readlane64(__builtin_bit_cast(uint64_t, v), src));
+__device__ __forceinline__ double shfl_f64(double v, int from) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    const uint32_t lo = __shfl((int)(uint32_t)u, from), hi = __shfl((int)(uint32_t)(u >> 32), from);
+    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
-__device__ __forceinline__ double wave_max_f64(double v) {
-    for (int s = 1; s < kWave; s <<= 1) {
-        const double o = shfl_xor_f64(v, s);
-        v = o > v ? o : v;
+// VPL logits that start on a boundary of their own size (or of 16 bytes where they are more).
+template <int VPL, bool BF16>
+__device__ __forceinline__ void load_logits(const void *p, int64_t i, float (&out)[VPL]) {
+    if constexpr (BF16) {
+        const uint16_t *src = static_cast<const uint16_t *>(p) + i;
+        constexpr int W = VPL < 8 ? VPL : 8;
+        typedef uint16_t vec __attribute__((ext_vector_type(W)));
+#pragma unroll
+        for (int k = 0; k < VPL; k += W) {
+            const vec v = *reinterpret_cast<const vec *>(src + k);
+#pragma unroll
+            for (int u = 0; u < W; ++u) out[k + u] = __uint_as_float((uint32_t)v[u] << 16);
+        }
+    } else {
+        const float *src = static_cast<const float *>(p) + i;
+        constexpr int W = VPL < 4 ? VPL : 4;
+        typedef float vec __attribute__((ext_vector_type(W)));
+#pragma unroll
+        for (int k = 0; k < VPL; k += W) {
+            const vec v = *reinterpret_cast<const vec *>(src + k);
+#pragma unroll
+            for (int u = 0; u < W; ++u) out[k + u] = v[u];
+        }
     }
-    return v;
 }
 
-__device__ __forceinline__ double wave_sum_f64(double v) {
-    for (int s = 1; s < kWave; s <<= 1) v += shfl_xor_f64(v, s);
-    return v;
+template <int VPL, bool BF16>
+__device__ __forceinline__ void store_logits(void *p, int64_t i, const float (&v)[VPL]) {
+    if constexpr (BF16 && VPL == 1) {
+        static_cast<uint16_t *>(p)[i] = (uint16_t)pack_bf16(v[0], 0.0f);
+    } else if constexpr (BF16) {
+        constexpr int W = VPL < 8 ? VPL / 2 : 4;
+        typedef uint32_t vec __attribute__((ext_vector_type(W)));
+#pragma unroll
+        for (int k = 0; k < VPL; k += 2 * W) {
+            vec w;
+#pragma unroll
+            for (int u = 0; u < W; ++u) w[u] = pack_bf16(v[k + 2 * u], v[k + 2 * u + 1]);
+            *reinterpret_cast<vec *>(static_cast<uint16_t *>(p) + i + k) = w;
+        }
+    } else {
+        constexpr int W = VPL < 4 ? VPL : 4;
+        typedef float vec __attribute__((ext_vector_type(W)));
+#pragma unroll
+        for (int k = 0; k < VPL; k += W) {
+            vec w;
+#pragma unroll
+            for (int u = 0; u < W; ++u) w[u] = v[k + u];
+            *reinterpret_cast<vec *>(static_cast<float *>(p) + i + k) = w;
+        }
+    }
 }
 
-__device__ __forceinline__ float wave_max_f32(float v) {
-    for (int s = 1; s < kWave; s <<= 1) v = fmaxf(v, __shfl_xor(v, s));
-    return v;
-}
-
-__device__ __forceinline__ float wave_sum_f32(float v) {
-    for (int s = 1; s < kWave; s <<= 1) v += __shfl_xor(v, s);
-    return v;
+// Orders LDS accesses of the wave's own lanes among each other (they are served in order).
+__device__ __forceinline__ void wave_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
 }
 
 // NaN and +inf: not a logit (or bias) the router can use.
 __device__ __forceinline__ bool unusable(float v) { return !(v < INFINITY); }
 
-template <int VPL, bool BF16>
-__global__ __launch_bounds__(kRouteWaves *kWave) void route_kernel(RouteParams p) {
-    const int lane = threadIdx.x & (kWave - 1);
-    const int64_t t = (int64_t)blockIdx.x * kRouteWaves + (threadIdx.x >> 6);
-    if (t >= p.T) return;  // whole wave leaves together
-    int64_t *idx_out = p.a.topk_idx + t * p.K;
-    float *w_out = p.a.topk_w + t * p.K;
-    if (p.a.token_mask != nullptr && p.a.token_mask[t] == 0) {
-        if (lane < p.K) {
-            idx_out[lane] = -1;
-            w_out[lane] = 0.0f;
-        }
-        return;
-    }
-    const double none = -INFINITY;
-    const int e0 = lane * VPL;
-    float logit[VPL];
-    bool bad = false;
-    float top = -INFINITY;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        float l = -INFINITY;
-        if (e0 + i < p.E) l = load_logit<BF16>(p.a.logits, t * p.a.stride + e0 + i);
-        if (unusable(l)) {
-            bad = true;
-            l = -INFINITY;
-        }
-        logit[i] = l;
-        top = fmaxf(top, l);
-    }
-    top = wave_max_f32(top);
+// How far apart two f32 choices have to be for their order to be sure, relative to 1 + their size.
+// With u = 2^-24: an exponential is off by (|argument| + 2) u of it at most, which for the argument
+// l - max of a softmax is under 2 u of 1, and for a sigmoid (whose argument is exact) under 2 u of the
+// score; sum and quotient of a sigmoid add 2 u, the bias u of the choice.  A softmax divides by a sum
+// whose terms are off by the same and whose 38 additions at most by u each: under 60 u.  Twice that
+// for two sides, and half as much again to spare.
+constexpr float kSigmoidSlack = 16 * 0x1p-24f, kSoftmaxSlack = 180 * 0x1p-24f;
 
-    // choice[i]: c_e; key[i]: what orders the experts (c_e, or the logit when there is no bias)
-    double choice[VPL], sum = 0.0;
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        choice[i] = 0.0;
-        if (logit[i] > -INFINITY) {
-            const double l = logit[i];
-            choice[i] = p.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top);
+// f32 to an integer that orders as it does (+0 and -0 alike); kNone is below all of them.
+constexpr int kNone = INT_MIN;
+__device__ __forceinline__ int order_of(float v) {
+    const int b = __float_as_int(v + 0.0f);
+    return b ^ ((b >> 31) & INT_MAX);
+}
+__device__ __forceinline__ float value_of(int o) { return __int_as_float(o ^ ((o >> 31) & INT_MAX)); }
+
+// Largest value over a token's LPT lanes, for all of them.
+template <int LPT>
+__device__ __forceinline__ int token_max(int v) {
+    if constexpr (LPT == kWave) {
+#define EP_MAX_STEP(ctrl, rows) \
+    { const int o = __builtin_amdgcn_update_dpp(v, v, ctrl, rows, 0xf, false); v = o > v ? o : v; }
+        EP_MAX_STEP(0x111, 0xf)  // row_shr:1
+        EP_MAX_STEP(0x112, 0xf)  // row_shr:2
+        EP_MAX_STEP(0x114, 0xf)  // row_shr:4
+        EP_MAX_STEP(0x118, 0xf)  // row_shr:8
+        EP_MAX_STEP(0x142, 0xa)  // row_bcast:15 into rows 1, 3
+        EP_MAX_STEP(0x143, 0xc)  // row_bcast:31 into rows 2, 3
+#undef EP_MAX_STEP
+        return readlane32(v, kWave - 1);
+    } else {
+        static_assert(LPT == 16, "a row of 16 lanes");
+        int o = (int)lane_xor<1>((uint32_t)v);
+        v = o > v ? o : v;
+        o = (int)lane_xor<2>((uint32_t)v);
+        v = o > v ? o : v;
+        o = (int)lane_xor<4>((uint32_t)v);
+        v = o > v ? o : v;
+        o = (int)lane_xor<8>((uint32_t)v);
+        return o > v ? o : v;
+    }
+}
+
+template <int LPT>
+__device__ __forceinline__ float token_sum(float v) {
+    for (int s = 1; s < LPT; s <<= 1) v += __shfl_xor(v, s);
+    return v;
+}
+template <int LPT>
+__device__ __forceinline__ double token_sum(double v) {
+    for (int s = 1; s < LPT; s <<= 1) v += shfl_xor_f64(v, s);
+    return v;
+}
+// The same for doubles, ordered as 64-bit integers in two halves: the largest high half, then the
+// largest low half among the lanes that have it.
+template <int LPT>
+__device__ __forceinline__ double token_max(double v) {
+    const int64_t b = __builtin_bit_cast(int64_t, v + 0.0);
+    const int64_t o = b ^ ((b >> 63) & INT64_MAX);
+    const int hi = token_max<LPT>((int)(o >> 32));
+    const int lo = token_max<LPT>((int)(o >> 32) == hi ? (int)((uint32_t)o ^ 0x80000000u) : INT_MIN);
+    const int64_t m = ((int64_t)hi << 32) | ((uint32_t)lo ^ 0x80000000u);
+    return __builtin_bit_cast(double, m ^ ((m >> 63) & INT64_MAX));
+}
+
+// The token's lanes of a ballot, in its low bits.
+template <int LPT>
+__device__ __forceinline__ uint64_t token_bits(uint64_t ballot, int lane) {
+    if constexpr (LPT == kWave) return ballot;
+    return (ballot >> (lane & (kWave - LPT))) & ((1ull << LPT) - 1ull);
+}
+
+// A lane's part of its token.
+template <int VPL>
+struct Part {
+    float logit[VPL];  // -inf: not to be chosen, whatever the bias
+    float bias[VPL];   // -inf: not to be chosen
+    int first;         // expert of element 0
+};
+
+// Which groups stay, as a bit each (a rating orders as `exact` or `rough` does, ties to the lower
+// group), from lane g's rating of group g.  Returns in *close whether a group kept and one dropped
+// are within `slack` of each other.
+template <int LPT, typename F>
+__device__ __forceinline__ uint64_t keep_groups(F rating, int G, int kept, float slack, int lane, bool *close) {
+    const int at = lane & (LPT - 1), base = lane & (kWave - LPT);
+    auto rating_of = [&](int g) {
+        if constexpr (sizeof(F) == 8)
+            return LPT == kWave ? __builtin_bit_cast(double, readlane64(__builtin_bit_cast(uint64_t, rating), g))
+                                : shfl_f64(rating, base + g);
+        else
+            return LPT == kWave ? readlanef(rating, g) : __shfl(rating, base + g);
+    };
+    int ahead = 0;  // groups rated above the lane's
+    for (int g = 0; g < G; ++g) {
+        const F o = rating_of(g);
+        ahead += o > rating || (o == rating && g < at);
+    }
+    const bool stays = at < G && ahead < kept;
+    const uint64_t bits = token_bits<LPT>(ballot64(stays), lane);
+    if (close != nullptr) {
+        bool near = false;
+        for (int g = 0; g < G; ++g) {
+            const float o = (float)rating_of(g), r = (float)rating;
+            // -inf (a group without experts to choose) is near nothing
+            near |= at < G && ((bits >> g) & 1ull) != (uint64_t)stays && fabsf(o - r) <= slack * (1.0f + fabsf(r));
         }
-        sum += choice[i];
+        *close = token_bits<LPT>(ballot64(near), lane) != 0ull;
     }
-    if (!p.sigmoid) {
-        sum = wave_sum_f64(sum);
+    return bits;
+}
+
+// A slot's expert (-1: none) and what it was chosen by.
+struct Chosen {
+    int expert, key;
+};
+
+// The choice in f32 for the token whose logits start at element `row`.  chosen (LDS): the slots, all
+// without an expert before, and one behind them.  Returns whether some token of the wave needs
+// choose_exact.
+template <int LPT, int VPL, bool BF16>
+__device__ __forceinline__ bool choose(const RouteParams &p, const Part<VPL> &t, int64_t row, int lane,
+                                       Chosen *chosen) {
+    const int at = lane & (LPT - 1);
+    const bool biased = p.a.bias != nullptr;
+    const bool by_logit = !biased && p.best == 1;  // what rates a group
+    const float slack = p.sigmoid ? kSigmoidSlack : kSoftmaxSlack;
+    float choice[VPL];
+    int key[VPL];
+    bool close = false;
+    if (biased || (p.G > 1 && !by_logit)) {
+        float top = 0.0f, sum = 1.0f;
+        if (!p.sigmoid) {
+            int m = kNone;
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) choice[i] /= sum;
+            for (int i = 0; i < VPL; ++i) {
+                const int o = t.logit[i] > -INFINITY ? order_of(t.logit[i]) : kNone;
+                m = o > m ? o : m;
+            }
+            m = token_max<LPT>(m);
+            top = m == kNone ? 0.0f : value_of(m);
+            sum = 0.0f;
+        }
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            choice[i] = p.sigmoid ? 1.0f / (1.0f + expf(-t.logit[i])) : expf(t.logit[i] - top);  // -inf: 0
+            sum += choice[i];
+        }
+        float scale = 1.0f;
+        if (!p.sigmoid) scale = 1.0f / token_sum<LPT>(sum);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) choice[i] = __builtin_fmaf(choice[i], scale, biased ? t.bias[i] : 0.0f);
     }
-    double key[VPL];
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
-        key[i] = logit[i];
-        if (p.a.bias != nullptr) {
-            float b = e0 + i < p.E ? p.a.bias[e0 + i] : -INFINITY;
-            if (unusable(b)) {
-                bad = true;
-                b = -INFINITY;
+        const bool able = t.logit[i] > -INFINITY && (!biased || t.bias[i] > -INFINITY);
+        key[i] = able ? order_of(biased ? choice[i] : t.logit[i]) : kNone;
+    }
+    if (p.G > 1) {
+        float rating = -INFINITY;  // lane g: of group g
+        auto best_two = [&](int lo, int hi, int &a, int &b) {
+            a = b = kNone;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                const int e = t.first + i;
+                const int v = e >= lo && e < hi && key[i] != kNone ? order_of(by_logit ? t.logit[i] : choice[i]) : kNone;
+                const int low = v < a ? v : a;
+                a = v > a ? v : a;
+                b = low > b ? low : b;
             }
-            if (b == -INFINITY) key[i] = none;
-            choice[i] += (double)b;
-            if (key[i] > none) key[i] = choice[i];
+        };
+        auto join = [&](int &a, int &b, int oa, int ob) {
+            const int low = a < oa ? a : oa;
+            a = a > oa ? a : oa;
+            b = b > ob ? b : ob;
+            b = b > low ? b : low;
+        };
+        auto rate = [&](int a, int b) {
+            if (a == kNone) return -INFINITY;
+            return p.best == 2 && b != kNone ? value_of(a) + value_of(b) : value_of(a);
+        };
+        const int lanes = p.group_size / VPL;  // lanes that share a group, where groups are whole lanes
+        if (p.group_size % VPL == 0 && (lanes & (lanes - 1)) == 0) {
+            const int lo = t.first / p.group_size * p.group_size;
+            int a, b;
+            best_two(lo, lo + p.group_size, a, b);
+            for (int s = 1; s < lanes; s <<= 1) join(a, b, __shfl_xor(a, s), __shfl_xor(b, s));
+            rating = rate(a, b);
+            const int from = at * lanes;  // a lane of group `at`
+            rating = __shfl(rating, (lane & (kWave - LPT)) + (from & (LPT - 1)));
+            if (at >= p.G) rating = -INFINITY;
+        } else {
+            for (int g = 0; g < p.G; ++g) {
+                int a, b;
+                best_two(g * p.group_size, (g + 1) * p.group_size, a, b);
+                for (int s = 1; s < LPT; s <<= 1) join(a, b, __shfl_xor(a, s), __shfl_xor(b, s));
+                if (at == g) rating = rate(a, b);
+            }
+        }
+        const uint64_t keep = keep_groups<LPT>(rating, p.G, p.kept, 2.0f * slack, lane, by_logit ? nullptr : &close);
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const int g = (t.first + i) / p.group_size;
+            if (g >= p.G || ((keep >> g) & 1ull) == 0ull) key[i] = kNone;
+        }
+    }
+    // num_topk rounds: the largest key left, lowest expert first; and one more, to see how near it is
+    const int rounds = p.K + (biased ? 1 : 0);
+    for (int j = 0; j < rounds; ++j) {
+        int m = key[0];
+#pragma unroll
+        for (int i = 1; i < VPL; ++i) m = key[i] > m ? key[i] : m;
+        const int best = token_max<LPT>(m);
+        if (ballot64(best != kNone) == 0ull) break;
+        const uint64_t holders = token_bits<LPT>(ballot64(m == best && best != kNone), lane);
+        const bool mine = holders != 0ull && at == __builtin_ctzll(holders | (1ull << 63));
+        int e = 0;
+        bool done = !mine;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            const bool hit = !done && key[i] == best;
+            key[i] = hit ? kNone : key[i];
+            e = hit ? i : e;
+            done |= hit;
+        }
+        if (mine) chosen[j] = {t.first + e, best};
+    }
+    if (biased) {
+        // lane j: slots j and j + 1.  The same logit and bias are a tie in any precision
+        wave_lds_order();
+        for (int j = at; j < p.K; j += LPT) {
+            const Chosen a = chosen[j], b = chosen[j + 1];
+            if (b.expert < 0) continue;
+            const float v = value_of(a.key);
+            if (v - value_of(b.key) > slack * (1.0f + fabsf(v))) continue;
+            close |= load_logit<BF16>(p.a.logits, row + a.expert) != load_logit<BF16>(p.a.logits, row + b.expert) ||
+                     p.a.bias[a.expert] != p.a.bias[b.expert];
+        }
+    }
+    return ballot64(close) != 0ull;
+}
+
+// The same in binary64 throughout, for waves with near ties: few, so it is written to take few
+// registers.  choice (LDS): the lane's VPL values, kWave apart.  on: the token is routed.
+template <int LPT, int VPL, bool BF16>
+__device__ __forceinline__ void choose_exact(const RouteParams &p, int64_t row, bool on, int lane, double *choice,
+                                             Chosen *chosen) {
+    const int at = lane & (LPT - 1), first = at * VPL;
+    const bool biased = p.a.bias != nullptr;
+    const double none = -INFINITY;
+    auto logit_of = [&](int i) {
+        if (!on || first + i >= p.E) return -INFINITY;
+        const float l = load_logit<BF16>(p.a.logits, row + first + i);
+        return unusable(l) ? -INFINITY : l;
+    };
+    float top = -INFINITY;
+#pragma unroll 1
+    for (int i = 0; i < VPL; ++i) top = fmaxf(top, logit_of(i));
+    for (int s = 1; s < LPT; s <<= 1) top = fmaxf(top, __shfl_xor(top, s));
+    double sum = 0.0;
+#pragma unroll 1
+    for (int i = 0; i < VPL; ++i) {
+        const float l = logit_of(i);
+        double c = 0.0;
+        if (l > -INFINITY) c = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)top);
+        choice[i * kWave] = c;
+        sum += c;
+    }
+    sum = p.sigmoid ? 1.0 : token_sum<LPT>(sum);
+#pragma unroll 1
+    for (int i = 0; i < VPL; ++i) {
+        double c = choice[i * kWave] / sum;
+        bool able = logit_of(i) > -INFINITY;
+        if (biased && able) {
+            const float b = p.a.bias[first + i];
+            able = b > -INFINITY && !unusable(b);
+            c += (double)b;
+        }
+        choice[i * kWave] = able ? c : none;
+    }
+    if (p.G > 1) {
+        double rating = none;
+        auto best_two = [&](int lo, int hi, double &a, double &b) {
+            a = b = none;
+#pragma unroll 1
+            for (int i = 0; i < VPL; ++i) {
+                const double v = first + i >= lo && first + i < hi ? choice[i * kWave] : none;
+                b = v > a ? a : v > b ? v : b;
+                a = v > a ? v : a;
+            }
+        };
+        auto join = [&](double &a, double &b, int s) {
+            const double oa = shfl_xor_f64(a, s), ob = shfl_xor_f64(b, s);
+            const double low = a < oa ? a : oa;
+            a = a > oa ? a : oa;
+            b = b > ob ? b : ob;
+            b = b > low ? b : low;
+        };
+        const int lanes = p.group_size / VPL;  // as in choose()
+        double a, b;
+        if (p.group_size % VPL == 0 && (lanes & (lanes - 1)) == 0) {
+            const int lo = first / p.group_size * p.group_size;
+            best_two(lo, lo + p.group_size, a, b);
+            for (int s = 1; s < lanes; s <<= 1) join(a, b, s);
+            rating = shfl_f64(p.best == 2 && b > none ? a + b : a, (lane & (kWave - LPT)) + ((at * lanes) & (LPT - 1)));
+            if (at >= p.G) rating = none;
+        } else {
+#pragma unroll 1
+            for (int g = 0; g < p.G; ++g) {
+                best_two(g * p.group_size, (g + 1) * p.group_size, a, b);
+                for (int s = 1; s < LPT; s <<= 1) join(a, b, s);
+                if (at == g) rating = p.best == 2 && b > none ? a + b : a;
+            }
+        }
+        const uint64_t keep = keep_groups<LPT>(rating, p.G, p.kept, 0.0f, lane, nullptr);
+#pragma unroll 1
+        for (int i = 0; i < VPL; ++i) {
+            const int g = (first + i) / p.group_size;
+            if (g >= p.G || ((keep >> g) & 1ull) == 0ull) choice[i * kWave] = none;
+        }
+    }
+    if (!biased) {
+#pragma unroll 1
+        for (int i = 0; i < VPL; ++i)
+            if (choice[i * kWave] > none) choice[i * kWave] = (double)logit_of(i);
+    }
+#pragma unroll 1
+    for (int j = 0; j < p.K; ++j) {
+        double m = none;
+        int e = 0;
+#pragma unroll 1
+        for (int i = 0; i < VPL; ++i) {
+            const double v = choice[i * kWave];
+            if (v > m) {
+                m = v;
+                e = i;
+            }
+        }
+        const double best = token_max<LPT>(m);
+        const uint64_t holders = token_bits<LPT>(ballot64(m == best && best > none), lane);
+        if (holders != 0ull && at == __builtin_ctzll(holders | (1ull << 63))) {
+            choice[e * kWave] = none;
+            chosen[j].expert = first + e;
+        }
+    }
+}
+
+template <int LPT, int VPL, bool BF16>
+__global__ __launch_bounds__(kRouteWaves *kWave) void route_kernel(RouteParams p) {
+    constexpr int kTokens = kWave / LPT;  // of a wave
+    __shared__ Chosen s_chosen[kRouteWaves * kTokens][kMaxTopk + 1];
+    __shared__ double s_exact[kRouteWaves][VPL][kWave];
+    const int lane = threadIdx.x & (kWave - 1), at = lane & (LPT - 1);
+    const int slot = threadIdx.x / LPT;  // the token's place in the block
+    const int64_t t = (int64_t)blockIdx.x * kRouteWaves * kTokens + slot;
+    const bool here = t < p.T;
+    const bool on = here && (p.a.token_mask == nullptr || p.a.token_mask[t] != 0);
+    const int64_t row = t * p.a.stride;
+    Part<VPL> part;
+    part.first = at * VPL;
+    bool bad = false;
+    if (p.vector) {  // a lane's logits are whole aligned words, and all of them in or out
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) part.logit[i] = -INFINITY;
+        if (on && part.first < p.E) load_logits<VPL, BF16>(p.a.logits, row + part.first, part.logit);
+    } else {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            part.logit[i] = -INFINITY;
+            if (on && part.first + i < p.E) part.logit[i] = load_logit<BF16>(p.a.logits, row + part.first + i);
+        }
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        part.bias[i] = 0.0f;
+        if (p.a.bias != nullptr && part.first + i < p.E) part.bias[i] = p.a.bias[part.first + i];
+    }
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        if (unusable(part.logit[i])) {
+            bad = true;
+            part.logit[i] = -INFINITY;
+        }
+        if (unusable(part.bias[i])) {
+            bad |= on;
+            part.bias[i] = -INFINITY;
         }
     }
     if (ballot64(bad) != 0ull && lane == 0) flag(p.a.dev_status, EP_DEV_BAD_LOGIT);
 
-    if (p.G > 1) {
-        // lane g: rating of group g
-        double rating = none;
-        for (int g = 0; g < p.G; ++g) {
-            const int lo = g * p.group_size, hi = lo + p.group_size;
-            const bool by_logit = p.best == 1 && p.a.bias == nullptr;
-            double a = none, b = none;  // the two largest of this lane's part of the group
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                if (e0 + i >= lo && e0 + i < hi && key[i] > none) {
-                    const double v = by_logit ? key[i] : choice[i];
-                    if (v > a) {
-                        b = a;
-                        a = v;
-                    } else if (v > b) {
-                        b = v;
-                    }
-                }
-            }
-            for (int s = 1; s < kWave; s <<= 1) {
-                const double oa = shfl_xor_f64(a, s), ob = shfl_xor_f64(b, s);
-                const double low = a < oa ? a : oa;
-                a = a > oa ? a : oa;
-                b = b > ob ? b : ob;
-                b = b > low ? b : low;
-            }
-            const double r = p.best == 2 && b > none ? a + b : a;
-            if (lane == g) rating = r;
-        }
-        int ahead = 0;  // groups rated above lane's group
-        for (int g = 0; g < p.G; ++g) {
-            const double o = readlane_f64(rating, g);
-            ahead += o > rating || (o == rating && g < lane);
-        }
-        const uint64_t keep = ballot64(lane < p.G && ahead < p.kept);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const int g = (e0 + i) / p.group_size;
-            if (g >= kWave || ((keep >> g) & 1ull) == 0ull) key[i] = none;
-        }
+    auto clear = [&] {
+        for (int j = at; j <= p.K; j += LPT) s_chosen[slot][j] = {-1, kNone};
+        wave_lds_order();
+    };
+    clear();
+    if (choose<LPT, VPL, BF16>(p, part, row, lane, s_chosen[slot])) {
+        wave_lds_order();
+        clear();
+        choose_exact<LPT, VPL, BF16>(p, row, on, lane, &s_exact[threadIdx.x / kWave][0][lane], s_chosen[slot]);
     }
+    wave_lds_order();
 
-    // num_topk rounds: the largest key left, lowest expert first; lane j keeps round j's expert
-    int chosen = -1;
-    for (int j = 0; j < p.K; ++j) {
-        double m = none;
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) m = key[i] > m ? key[i] : m;
-        const double best = wave_max_f64(m);
-        if (!(best > none)) break;
-        const int owner = __builtin_ctzll(ballot64(m == best));
-        int e = -1;
-#pragma unroll
-        for (int i = VPL - 1; i >= 0; --i)
-            if (key[i] == best) e = i;
-        e = readlane32(e, owner);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (lane == owner && i == e) key[i] = none;
-        if (lane == j) chosen = owner * VPL + e;
-    }
-
+    // lane j: slot j (num_topk <= LPT, which the launcher sees to).  In 64 bits: there are few of them
+    const int chosen = at < p.K ? s_chosen[slot][at].expert : -1;
     double s = 0.0;
     if (chosen >= 0) {
-        const double l = load_logit<BF16>(p.a.logits, t * p.a.stride + chosen);
-        s = p.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - (double)top) / sum;
+        const double l = load_logit<BF16>(p.a.logits, row + chosen);
+        s = p.sigmoid ? 1.0 / (1.0 + exp(-l)) : l;
+    }
+    if (!p.sigmoid) {
+        // relative to the largest logit of the row, or of the chosen ones where only their ratios count
+        double ref = chosen >= 0 ? s : -INFINITY, sum = 1.0;
+        if (p.renorm) {
+            ref = token_max<LPT>(ref);
+        } else {
+            int m = kNone;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                const int o = part.logit[i] > -INFINITY ? order_of(part.logit[i]) : kNone;
+                m = o > m ? o : m;
+            }
+            m = token_max<LPT>(m);
+            const float top = m == kNone ? 0.0f : value_of(m);
+            float all = 0.0f;
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) all += expf(part.logit[i] - top);
+            ref = (double)top;
+            sum = (double)token_sum<LPT>(all);
+        }
+        s = chosen >= 0 ? exp(s - ref) / sum : 0.0;
     }
     double w = s * (double)p.scale;
     if (p.renorm) {
-        const double all = wave_sum_f64(s);
+        const double all = token_sum<LPT>(s);
         w = all > 0.0 ? w / all : 0.0;
     }
-    if (lane < p.K) {
-        idx_out[lane] = chosen;
-        w_out[lane] = (float)w;
+    if (here && at < p.K) {
+        p.a.topk_idx[t * p.K + at] = chosen;
+        p.a.topk_w[t * p.K + at] = (float)w;
     }
 }
 
-template <int VPL, bool BF16>
+// VPL experts a lane at a time, all of a token's at once where they fit.
+template <int LPT, int VPL, bool BF16>
 __global__ __launch_bounds__(kRouteWaves *kWave) void route_backward_kernel(RouteBackwardParams p) {
-    const int lane = threadIdx.x & (kWave - 1);
-    const int64_t t = (int64_t)blockIdx.x * kRouteWaves + (threadIdx.x >> 6);
-    if (t >= p.T) return;  // whole wave leaves together
-    const int e0 = lane * VPL;
+    constexpr int kTokens = kWave / LPT, kSpan = LPT * VPL;
+    const int lane = threadIdx.x & (kWave - 1), at = lane & (LPT - 1), base = lane & (kWave - LPT);
+    const int64_t t = (int64_t)blockIdx.x * kRouteWaves * kTokens + threadIdx.x / LPT;
+    const bool here = t < p.T;
+    const int64_t row = t * p.a.stride;
     float logit[VPL];
     bool bad = false;
-    float top = -INFINITY;
+    auto load = [&](int from) {  // -inf where there is no usable logit
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        float l = -INFINITY;
-        if (e0 + i < p.E) l = load_logit<BF16>(p.a.logits, t * p.a.stride + e0 + i);
-        if (unusable(l)) {
-            bad = true;
-            l = -INFINITY;
+        for (int i = 0; i < VPL; ++i) logit[i] = -INFINITY;
+        const int e = from + at * VPL;
+        if (p.vector) {  // a lane's logits are whole aligned words, and all of them in or out
+            if (here && e < p.E) load_logits<VPL, BF16>(p.a.logits, row + e, logit);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (here && e + i < p.E) logit[i] = load_logit<BF16>(p.a.logits, row + e + i);
         }
-        logit[i] = l;
-        top = fmaxf(top, l);
-    }
-    top = wave_max_f32(top);
-    float score[VPL], sum = 0.0f;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        score[i] = 0.0f;
-        if (logit[i] > -INFINITY) score[i] = p.sigmoid ? 1.0f / (1.0f + expf(-logit[i])) : expf(logit[i] - top);
-        sum += score[i];
-    }
+        for (int i = 0; i < VPL; ++i) {
+            if (unusable(logit[i])) {
+                bad = true;
+                logit[i] = -INFINITY;
+            }
+        }
+    };
+    // softmax: the largest logit and the sum relative to it
+    float top = 0.0f, sum = 1.0f;
+    load(0);
     if (!p.sigmoid) {
-        sum = wave_sum_f32(sum);
+        int m = kNone;
+        for (int from = 0; from < p.E; from += kSpan) {
+            if (from > 0) load(from);
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) score[i] = sum > 0.0f ? score[i] / sum : 0.0f;
+            for (int i = 0; i < VPL; ++i) {
+                const int o = logit[i] > -INFINITY ? order_of(logit[i]) : kNone;
+                m = o > m ? o : m;
+            }
+        }
+        m = token_max<LPT>(m);
+        top = m == kNone ? 0.0f : value_of(m);
+        sum = 0.0f;
+        for (int from = 0; from < p.E; from += kSpan) {
+            if (p.E > kSpan) load(from);
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) sum += expf(logit[i] - top);
+        }
+        sum = token_sum<LPT>(sum);
     }
 
     // lane j: slot j's expert, its score and the gradient of that score, in 64 bits: the sums over
-    // the slots cancel
-    int64_t id = -1;
+    // the slots cancel (num_topk <= LPT, which the launcher sees to)
+    int id = -1;
     double s = 0.0, g = 0.0;
     bool bad_id = false;
-    if (lane < p.K) {
-        id = p.a.topk_idx[t * p.K + lane];
-        if (id < -1 || id >= p.E) {
-            bad_id = true;
-            id = -1;
-        }
-        if (id >= 0) {
-            const float l = load_logit<BF16>(p.a.logits, t * p.a.stride + id);
+    if (here && at < p.K) {
+        const int64_t e = p.a.topk_idx[t * p.K + at];
+        bad_id = e < -1 || e >= p.E;
+        if (e >= 0 && e < p.E) {
+            id = (int)e;
+            const float l = load_logit<BF16>(p.a.logits, row + id);
             if (l > -INFINITY && !unusable(l))
                 s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)top) / (double)sum;
-            g = p.a.grad_w[t * p.K + lane];
+            g = p.a.grad_w[t * p.K + at];
         }
     }
-    if (ballot64(bad) != 0ull && lane == 0) flag(p.a.dev_status, EP_DEV_BAD_LOGIT);
     if (ballot64(bad_id) != 0ull && lane == 0) flag(p.a.dev_status, EP_DEV_BAD_TOPK_IDX);
     double ds = g * (double)p.scale;
     if (p.renorm) {
-        const double all = wave_sum_f64(s), gs = wave_sum_f64(id >= 0 ? g * s : 0.0);
+        const double all = token_sum<LPT>(s), gs = token_sum<LPT>(g * s);
         ds = id >= 0 && all > 0.0 ? (double)p.scale * (g - gs / all) / all : 0.0;
     }
     const float slot = (float)ds;
-    const float mean = p.sigmoid ? 0.0f : (float)wave_sum_f64(id >= 0 ? ds * s : 0.0);
+    const float mean = p.sigmoid ? 0.0f : (float)token_sum<LPT>(ds * s);
 
-    float d[VPL];
+    for (int from = 0; from < p.E; from += kSpan) {
+        if (p.E > kSpan) load(from);
+        const int e0 = from + at * VPL;
+        float d[VPL];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) d[i] = 0.0f;
-    for (int j = 0; j < p.K; ++j) {
-        const int e = readlane32((int)id, j);
-        const float v = readlanef(slot, j);
+        for (int i = 0; i < VPL; ++i) d[i] = 0.0f;
+        for (int j = 0; j < p.K; ++j) {
+            const int e = (LPT == kWave ? readlane32(id, j) : __shfl(id, base + j)) - e0;
+            const float v = LPT == kWave ? readlanef(slot, j) : __shfl(slot, base + j);
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)
-            if (e == e0 + i) d[i] += v;
-    }
-#pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        if (e0 + i >= p.E) continue;
-        float v = 0.0f;
-        if (logit[i] > -INFINITY) {
-            // 1 - s as its own sigmoid: it does not cancel where s is near 1
-            if (p.sigmoid)
-                v = d[i] * score[i] * (1.0f / (1.0f + expf(logit[i])));
-            else
-                v = score[i] * (d[i] - mean);
+            for (int i = 0; i < VPL; ++i)
+                if (e == i) d[i] += v;
         }
-        const int64_t at = t * p.a.grad_stride + e0 + i;
-        if constexpr (BF16)
-            static_cast<uint16_t *>(p.a.grad_logits)[at] = (uint16_t)pack_bf16(v, 0.0f);
-        else
-            static_cast<float *>(p.a.grad_logits)[at] = v;
+#pragma unroll
+        for (int i = 0; i < VPL; ++i) {
+            // sigmoid: 1 - s as its own sigmoid, which does not cancel where s is near 1
+            if (p.sigmoid)
+                d[i] = d[i] * (1.0f / (1.0f + expf(-logit[i]))) * (1.0f / (1.0f + expf(logit[i])));
+            else
+                d[i] = expf(logit[i] - top) / sum * (d[i] - mean);
+            if (logit[i] == -INFINITY) d[i] = 0.0f;
+        }
+        if (!here) continue;
+        const int64_t out = t * p.a.grad_stride + e0;
+        if (p.vector_out) {
+            if (e0 < p.E) store_logits<VPL, BF16>(p.a.grad_logits, out, d);
+        } else {
+#pragma unroll
+            for (int i = 0; i < VPL; ++i) {
+                if (e0 + i >= p.E) continue;
+                if constexpr (BF16)
+                    static_cast<uint16_t *>(p.a.grad_logits)[out + i] = (uint16_t)pack_bf16(d[i], 0.0f);
+                else
+                    static_cast<float *>(p.a.grad_logits)[out + i] = d[i];
+            }
+        }
     }
+    if (ballot64(bad) != 0ull && lane == 0) flag(p.a.dev_status, EP_DEV_BAD_LOGIT);
 }
 
+// Whether rows of E values `stride` apart from p let a lane move VPL of them as whole words.
 template <int VPL, bool BF16>
-void start(const RouteParams &p, hipStream_t stream) {
-    const unsigned blocks = (unsigned)((p.T + kRouteWaves - 1) / kRouteWaves);
-    hipLaunchKernelGGL((route_kernel<VPL, BF16>), dim3(blocks), dim3(kRouteWaves * kWave), 0, stream, p);
-}
-template <int VPL, bool BF16>
-void start(const RouteBackwardParams &p, hipStream_t stream) {
-    const unsigned blocks = (unsigned)((p.T + kRouteWaves - 1) / kRouteWaves);
-    hipLaunchKernelGGL((route_backward_kernel<VPL, BF16>), dim3(blocks), dim3(kRouteWaves * kWave), 0, stream, p);
+bool whole_words(const void *p, int64_t stride, int E) {
+    const int64_t size = BF16 ? 2 : 4, word = VPL * size, unit = word < 16 ? word : 16;
+    return E % VPL == 0 && reinterpret_cast<uintptr_t>(p) % unit == 0 && stride * size % unit == 0;
 }
 
-// The fewest experts a lane that hold E.
-template <typename P>
-hipError_t start_sized(const P &p, hipStream_t stream) {
-#define EP_ROUTE_CASE(V)                   \
-    if (p.E <= V * kWave) {                \
-        if (p.a.bf16)                      \
-            start<V, true>(p, stream);     \
-        else                               \
-            start<V, false>(p, stream);    \
-        return hipGetLastError();          \
-    }
-    EP_ROUTE_CASE(1)
-    EP_ROUTE_CASE(2)
-    EP_ROUTE_CASE(4)
-    EP_ROUTE_CASE(8)
-    EP_ROUTE_CASE(16)
-    EP_ROUTE_CASE(32)
-#undef EP_ROUTE_CASE
-    return hipErrorInvalidValue;
+template <int LPT, int VPL, bool BF16>
+hipError_t start(RouteParams p, hipStream_t stream) {
+    constexpr int kTokens = kRouteWaves * kWave / LPT;
+    p.vector = whole_words<VPL, BF16>(p.a.logits, p.a.stride, p.E);
+    hipLaunchKernelGGL((route_kernel<LPT, VPL, BF16>), dim3((unsigned)((p.T + kTokens - 1) / kTokens)),
+                       dim3(kRouteWaves * kWave), 0, stream, p);
+    return hipGetLastError();
+}
+template <int LPT, int VPL, bool BF16>
+hipError_t start(RouteBackwardParams p, hipStream_t stream) {
+    constexpr int kTokens = kRouteWaves * kWave / LPT;
+    p.vector = whole_words<VPL, BF16>(p.a.logits, p.a.stride, p.E);
+    p.vector_out = whole_words<VPL, BF16>(p.a.grad_logits, p.a.grad_stride, p.E);
+    hipLaunchKernelGGL((route_backward_kernel<LPT, VPL, BF16>), dim3((unsigned)((p.T + kTokens - 1) / kTokens)),
+                       dim3(kRouteWaves * kWave), 0, stream, p);
+    return hipGetLastError();
+}
+
+template <bool BF16>
+hipError_t start_route(const RouteParams &p, hipStream_t stream) {
+    const bool few = p.T < kManyTokens || p.K > 16 || p.G > 16;
+    if (!few && p.E <= 64) return start<16, 4, BF16>(p, stream);
+    if (!few && p.E <= 128) return start<16, 8, BF16>(p, stream);
+    if (!few && p.E <= 256) return start<16, 16, BF16>(p, stream);
+    if (p.E <= 64) return start<64, 1, BF16>(p, stream);
+    if (p.E <= 128) return start<64, 2, BF16>(p, stream);
+    if (p.E <= 256) return start<64, 4, BF16>(p, stream);
+    if (p.E <= 512) return start<64, 8, BF16>(p, stream);
+    if (p.E <= 1024) return start<64, 16, BF16>(p, stream);
+    return start<64, 32, BF16>(p, stream);
+}
+
+template <bool BF16>
+hipError_t start_backward(const RouteBackwardParams &p, hipStream_t stream) {
+    const bool few = p.T < kManyTokens || p.K > 16;
+    if (!few && p.E <= 64) return start<16, 4, BF16>(p, stream);
+    if (!few && p.E <= 128) return start<16, 8, BF16>(p, stream);
+    if (p.E <= 64) return start<64, 1, BF16>(p, stream);
+    if (p.E <= 128) return start<64, 2, BF16>(p, stream);
+    return start<64, 4, BF16>(p, stream);
 }
 
 }  // namespace
@@ -352,7 +742,7 @@ hipError_t launch_route(const ep_shape_t &s, const ep_router_t &r, const RouteAr
     p.sigmoid = r.score == EP_SCORE_SIGMOID;
     p.renorm = r.renormalize != 0;
     p.scale = r.weight_scale;
-    return start_sized(p, stream);
+    return a.bf16 ? start_route<true>(p, stream) : start_route<false>(p, stream);
 }
 
 hipError_t launch_route_backward(const ep_shape_t &s, const ep_router_t &r, const RouteBackwardArgs &a,
@@ -366,7 +756,7 @@ hipError_t launch_route_backward(const ep_shape_t &s, const ep_router_t &r, cons
     p.sigmoid = r.score == EP_SCORE_SIGMOID;
     p.renorm = r.renormalize != 0;
     p.scale = r.weight_scale;
-    return start_sized(p, stream);
+    return a.bf16 ? start_backward<true>(p, stream) : start_backward<false>(p, stream);
 }
 
 }  // namespace ep
