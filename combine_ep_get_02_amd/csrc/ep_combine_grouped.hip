@@ -13,7 +13,8 @@ typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
 struct Params {
     CombineGroupedArgs a;
     int64_t T, units;  // tokens; 16-byte units of a row
-    int E, R, K, segments;
+    int E, R, K;
+    int64_t segments;  // waves of a token's row
 };
 
 // Lane j < K: the grouped row of token t's slot j (-1 without one) and its weight.
@@ -51,109 +52,144 @@ __device__ __forceinline__ void report(const Params &p, int lane, int bad) {
 
 constexpr int kWaves = 4;
 
-// One wave per (token, segment of 64 * VPL 16-byte units).
-template <int VPL>
+// One wave per (token, segment of 64 16-byte units).  Up to kBatch rows' segments are loaded before
+// the first is used: a row at a time, a wave would wait out the memory's latency k times (prefill,
+// 4096 tokens of 8 rows of 7168: 88-93 us with 1 to 4 units a lane and batches of 2 to 8 alike, 5.7 to
+// 6.0 TB/s; 128 tokens: 8.8 us, 10 us a row at a time).
+constexpr int kBatch = 8;
 __global__ __launch_bounds__(kWaves *kWave) void combine_grouped_kernel(Params p) {
     const int lane = threadIdx.x & (kWave - 1);
     const int64_t w = (int64_t)blockIdx.x * kWaves + (threadIdx.x >> 6);
     if (w >= p.T * p.segments) return;  // whole wave leaves together
     const int64_t t = w / p.segments;
-    const int seg = (int)(w - t * p.segments);
+    const int64_t c = (w - t * p.segments) * kWave + lane;
     float weight;
     int bad;
     const int row = find_row(p, t, lane, &weight, &bad);
-    if (seg == 0) report(p, lane, bad);
-    const int64_t c0 = (int64_t)seg * VPL * kWave + lane;
-    const u32x4 *y = static_cast<const u32x4 *>(p.a.y);
+    if (w == t * p.segments) report(p, lane, bad);
+    const u32x4 *y = static_cast<const u32x4 *>(p.a.y) + c;
+    const bool inside = c < p.units;
 
-    float acc[VPL][8];
+    float acc[8];
 #pragma unroll
-    for (int i = 0; i < VPL; ++i)
+    for (int k = 0; k < 8; ++k) acc[k] = 0.0f;
+    uint64_t todo = ballot64(row >= 0);
+    while (todo != 0ull) {
+        u32x4 v[kBatch];
+        float wj[kBatch];
+        int n = 0;
 #pragma unroll
-        for (int k = 0; k < 8; ++k) acc[i][k] = 0.0f;
-    for (uint64_t todo = ballot64(row >= 0); todo != 0ull; todo &= todo - 1ull) {
-        const int j = __builtin_ctzll(todo);
-        const float wj = readlanef(weight, j);
-        const u32x4 *src = y + (int64_t)readlane32(row, j) * p.units + c0;
+        for (int u = 0; u < kBatch; ++u) {
+            if (todo == 0ull) break;
+            const int j = __builtin_ctzll(todo);
+            todo &= todo - 1ull;
+            wj[u] = readlanef(weight, j);
+            const u32x4 *src = y + (int64_t)readlane32(row, j) * p.units;
+            if (inside) v[u] = __builtin_nontemporal_load(src);
+            n = u + 1;
+        }
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            if (c0 + i * kWave < p.units) {
-                const u32x4 v = __builtin_nontemporal_load(src + i * kWave);
+        for (int u = 0; u < kBatch; ++u) {
+            if (u >= n) break;
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    acc[i][2 * k] = __builtin_fmaf(wj, bf16_low(v[k]), acc[i][2 * k]);
-                    acc[i][2 * k + 1] = __builtin_fmaf(wj, bf16_high(v[k]), acc[i][2 * k + 1]);
-                }
+            for (int k = 0; k < 4; ++k) {
+                acc[2 * k] = __builtin_fmaf(wj[u], bf16_low(v[u][k]), acc[2 * k]);
+                acc[2 * k + 1] = __builtin_fmaf(wj[u], bf16_high(v[u][k]), acc[2 * k + 1]);
             }
         }
     }
-    u32x4 *dst = static_cast<u32x4 *>(p.a.out) + t * p.units + c0;
+    u32x4 o;
 #pragma unroll
-    for (int i = 0; i < VPL; ++i) {
-        u32x4 o;
-#pragma unroll
-        for (int k = 0; k < 4; ++k) o[k] = pack_bf16(acc[i][2 * k], acc[i][2 * k + 1]);
-        if (c0 + i * kWave < p.units) __builtin_nontemporal_store(o, dst + i * kWave);
+    for (int k = 0; k < 4; ++k) o[k] = pack_bf16(acc[2 * k], acc[2 * k + 1]);
+    if (inside) __builtin_nontemporal_store(o, static_cast<u32x4 *>(p.a.out) + t * p.units + c);
+}
+
+// The padding rows among grouped rows blockIdx.x, blockIdx.x + gridDim.x, ... get zeros; each wave
+// looks at 64 of the block's rows at a time.
+template <int WAVES>
+__device__ __forceinline__ void zero_padding(const Params &p) {
+    const int lane = threadIdx.x & (kWave - 1);
+    u32x4 *gy = static_cast<u32x4 *>(p.a.out);
+    int64_t n = p.a.num_rows;
+    if (n > 0) n = *p.a.num_grouped < n ? *p.a.num_grouped : n;
+    const u32x4 zero = {0u, 0u, 0u, 0u};
+    for (int64_t first = (threadIdx.x >> 6) * kWave; blockIdx.x + first * gridDim.x < n; first += WAVES * kWave) {
+        const int64_t g = blockIdx.x + (first + lane) * gridDim.x;
+        uint64_t todo = ballot64(g < n && p.a.grouped_row[g] < 0);
+        for (; todo != 0ull; todo &= todo - 1ull) {
+            const int64_t r = blockIdx.x + (first + __builtin_ctzll(todo)) * gridDim.x;
+            for (int64_t c = lane; c < p.units; c += kWave) __builtin_nontemporal_store(zero, gy + r * p.units + c);
+        }
     }
 }
 
 // One block per token: the token's gradient row is scaled into each of its grouped rows, and its
-// product with that row's output summed over the block.  After its token a block zeroes the
-// padding rows among grouped rows blockIdx.x, blockIdx.x + gridDim.x, ...
-__global__ __launch_bounds__(kWaves *kWave) void combine_grouped_backward_kernel(Params p) {
-    __shared__ float s_dot[kMaxTopk][kWaves];
+// product with that row's output summed over the block.  The gradient row stays in registers, UPT
+// 16-byte units a thread (rows of up to 64 WAVES UPT units; longer ones in turns), and the next row's
+// outputs are loaded while one is worked on.
+template <int WAVES, int UPT>
+__global__ __launch_bounds__(WAVES *kWave) void combine_grouped_backward_kernel(Params p) {
+    __shared__ float s_dot[kMaxTopk][WAVES];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = threadIdx.x >> 6;
     const int64_t t = blockIdx.x;
-    const u32x4 *y = static_cast<const u32x4 *>(p.a.y);
-    u32x4 *gy = static_cast<u32x4 *>(p.a.out);
     if (t < p.T) {
         float weight;
         int bad;
         const int row = find_row(p, t, lane, &weight, &bad);
         if (wave == 0) report(p, lane, bad);
-        const u32x4 *grad = static_cast<const u32x4 *>(p.a.grad) + t * p.units;
         const uint64_t there = ballot64(row >= 0);
-        for (uint64_t todo = there; todo != 0ull; todo &= todo - 1ull) {
-            const int j = __builtin_ctzll(todo);
-            const float wj = readlanef(weight, j);
-            const int64_t at = (int64_t)readlane32(row, j) * p.units;
-            float dot = 0.0f;
-            for (int64_t c = threadIdx.x; c < p.units; c += kWaves * kWave) {
-                const u32x4 v = __builtin_nontemporal_load(y + at + c);
-                const u32x4 g = grad[c];
-                u32x4 o;
+        float total = 0.0f;  // lane j: of slot j, this wave's part
+        for (int64_t from = 0; from < p.units; from += UPT * WAVES * kWave) {
+            const int64_t c0 = from + threadIdx.x;
+            const u32x4 *grad = static_cast<const u32x4 *>(p.a.grad) + t * p.units + c0;
+            const u32x4 *y = static_cast<const u32x4 *>(p.a.y) + c0;
+            u32x4 *gy = static_cast<u32x4 *>(p.a.out) + c0;
+            u32x4 g[UPT], v[UPT], next[UPT];
+            const u32x4 zero = {0u, 0u, 0u, 0u};
+            auto load = [&](u32x4(&to)[UPT], const u32x4 *src) {
 #pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    dot = __builtin_fmaf(bf16_low(v[k]), bf16_low(g[k]), dot);
-                    dot = __builtin_fmaf(bf16_high(v[k]), bf16_high(g[k]), dot);
-                    o[k] = pack_bf16(wj * bf16_low(g[k]), wj * bf16_high(g[k]));
+                for (int i = 0; i < UPT; ++i) {
+                    to[i] = zero;
+                    if (c0 + i * WAVES * kWave < p.units) to[i] = __builtin_nontemporal_load(src + i * WAVES * kWave);
                 }
-                __builtin_nontemporal_store(o, gy + at + c);
+            };
+            load(g, grad);
+            uint64_t todo = there;
+            if (todo != 0ull) load(next, y + (int64_t)readlane32(row, __builtin_ctzll(todo)) * p.units);
+            while (todo != 0ull) {
+                const int j = __builtin_ctzll(todo);
+                todo &= todo - 1ull;
+#pragma unroll
+                for (int i = 0; i < UPT; ++i) v[i] = next[i];
+                if (todo != 0ull) load(next, y + (int64_t)readlane32(row, __builtin_ctzll(todo)) * p.units);
+                const float wj = readlanef(weight, j);
+                u32x4 *dst = gy + (int64_t)readlane32(row, j) * p.units;
+                float dot = 0.0f;
+#pragma unroll
+                for (int i = 0; i < UPT; ++i) {
+                    u32x4 o;
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        dot = __builtin_fmaf(bf16_low(v[i][k]), bf16_low(g[i][k]), dot);
+                        dot = __builtin_fmaf(bf16_high(v[i][k]), bf16_high(g[i][k]), dot);
+                        o[k] = pack_bf16(wj * bf16_low(g[i][k]), wj * bf16_high(g[i][k]));
+                    }
+                    if (c0 + i * WAVES * kWave < p.units) __builtin_nontemporal_store(o, dst + i * WAVES * kWave);
+                }
+                for (int s = 1; s < kWave; s <<= 1) dot += __shfl_xor(dot, s);
+                if (lane == j) total += dot;
             }
-            for (int s = 1; s < kWave; s <<= 1) dot += __shfl_xor(dot, s);
-            if (lane == 0) s_dot[j][wave] = dot;
         }
+        if (lane < p.K) s_dot[lane][wave] = total;
         __syncthreads();
         if (wave == 0 && lane < p.K) {
             float dot = 0.0f;
-            if ((there >> lane) & 1ull)
-                for (int i = 0; i < kWaves; ++i) dot += s_dot[lane][i];
+            for (int i = 0; i < WAVES; ++i) dot += s_dot[lane][i];
             p.a.grad_w[t * p.K + lane] = dot;
         }
     }
-    // padding rows: each wave looks at 64 of the block's rows at a time
-    int64_t n = p.a.num_rows;
-    if (n > 0) n = *p.a.num_grouped < n ? *p.a.num_grouped : n;
-    const u32x4 zero = {0u, 0u, 0u, 0u};
-    for (int64_t first = (int64_t)wave * kWave; blockIdx.x + first * gridDim.x < n; first += kWaves * kWave) {
-        const int64_t g = blockIdx.x + (first + lane) * gridDim.x;
-        uint64_t todo = ballot64(g < n && p.a.grouped_row[g] < 0);
-        for (; todo != 0ull; todo &= todo - 1ull) {
-            const int64_t r = blockIdx.x + (first + __builtin_ctzll(todo)) * gridDim.x;
-            for (int64_t c = lane; c < p.units; c += kWave) gy[r * p.units + c] = zero;
-        }
-    }
+    zero_padding<WAVES>(p);
 }
 
 Params params(const ep_shape_t &s, const CombineGroupedArgs &a) {
@@ -173,10 +209,9 @@ Params params(const ep_shape_t &s, const CombineGroupedArgs &a) {
 hipError_t launch_combine_grouped(const ep_shape_t &s, const CombineGroupedArgs &a, hipStream_t stream) {
     if (s.num_tokens == 0) return hipSuccess;
     Params p = params(s, a);
-    constexpr int VPL = 2;
-    p.segments = (int)((p.units + VPL * kWave - 1) / (VPL * kWave));
+    p.segments = (p.units + kWave - 1) / kWave;
     const int64_t blocks = (p.T * p.segments + kWaves - 1) / kWaves;
-    hipLaunchKernelGGL((combine_grouped_kernel<VPL>), dim3((unsigned)blocks), dim3(kWaves * kWave), 0, stream, p);
+    hipLaunchKernelGGL(combine_grouped_kernel, dim3((unsigned)blocks), dim3(kWaves * kWave), 0, stream, p);
     return hipGetLastError();
 }
 
@@ -186,7 +221,15 @@ hipError_t launch_combine_grouped_backward(const ep_shape_t &s, const CombineGro
     int64_t blocks = a.num_rows / 16 < 1024 ? a.num_rows / 16 + 1 : 1024;
     if (p.T > blocks) blocks = p.T;
     if (p.T == 0 && a.num_rows == 0) return hipSuccess;
-    hipLaunchKernelGGL(combine_grouped_backward_kernel, dim3((unsigned)blocks), dim3(kWaves * kWave), 0, stream, p);
+    auto start = [&](auto kernel, int waves) {
+        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(waves * kWave), 0, stream, p);
+    };
+    // rows up to 4 KiB in one turn of four waves; wider ones take 8 waves of two units (16 KiB a turn):
+    // 4096-wide rows 292-300 us at 16384 tokens (5.3 TB/s), as 4 or 16 waves do
+    if (p.units <= 4 * kWave)
+        start(combine_grouped_backward_kernel<4, 1>, 4);
+    else
+        start(combine_grouped_backward_kernel<8, 2>, 8);
     return hipGetLastError();
 }
 
