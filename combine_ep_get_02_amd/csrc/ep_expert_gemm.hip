@@ -212,99 +212,160 @@ __global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(Gemm
                         b * kScaleBlock);
         load_to_lds(sbuf, reinterpret_cast<float *>(to + kS) + wave * kWave, sat, b * 4);
     };
-    auto multiply = [&](const u32x4 *from) {
-        const u32x4 *x = from + kX, *w = from + kW;
+    // the lane's units of any row it reads: 2 u + half, where the rotation has put them
+    const int unit0 = rotate(r32, half);
+    auto scales_of = [&](const u32x4 *from, int i, float (&scale)[2]) {
         const float *s = reinterpret_cast<const float *>(from + kS);
-        // the lane's units of any row it reads: 2 u + half, where the rotation has put them
-        int u0 = rotate(r32, half);
-        asm volatile("" : "+v"(u0));  // addresses are cheaper formed anew than kept in registers
-        auto unit_of = [&](const u32x4 *rows, int r, int u) { return rows[r * kUnits + (u0 ^ (2 * u))]; };
-        f16x8 fw[2][8];  // SWIGLU: the wave's weights as f16
-        i32x8 cw[2][2];  // otherwise: their codes
+        const int r = wm * 32 * MI + i * 32 + r32;
+        scale[0] = s[r] * s[BM + (SWIGLU ? 0 : wn >> 1)];
+        scale[1] = SWIGLU ? s[r] * s[BM + 1] : scale[0];
+    };
+    auto add = [&](f32x16 &sum, const f32x16 &part, float scale) {
 #pragma unroll
-        for (int j = 0; j < 2; ++j) {
+        for (int e = 0; e < 16; ++e) sum[e] = __builtin_fmaf(part[e], scale, sum[e]);
+    };
+    load(s_0, 0);
+    end_step();
+    if constexpr (SWIGLU) {
+        auto multiply = [&](const u32x4 *from) {
+            const u32x4 *x = from + kX, *w = from + kW;
+            int u0 = unit0;
+            asm volatile("" : "+v"(u0));  // addresses are cheaper formed anew than kept in registers
+            auto unit_of = [&](const u32x4 *rows, int r, int u) { return rows[r * kUnits + (u0 ^ (2 * u))]; };
+            f16x8 fw[2][8];  // the wave's weights
 #pragma unroll
-            for (int u = 0; u < 4; ++u) {
-                const u32x4 unit = unit_of(w, wn * 64 + j * 32 + r32, u);
-                if constexpr (SWIGLU) {
-                    fw[j][2 * u] = to_f16<0>(unit);
-                    fw[j][2 * u + 1] = to_f16<1>(unit);
-                } else {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) cw[j][u >> 1][(u & 1) * 4 + k] = (int)unit[k];
-                }
-            }
-        }
-#pragma unroll
-        for (int i = 0; i < MI; ++i) {
-            const int r = wm * 32 * MI + i * 32 + r32;
-            f32x16 part[2];
-#pragma unroll
-            for (int e = 0; e < 16; ++e) part[0][e] = part[1][e] = 0.0f;
-            if constexpr (SWIGLU) {
+            for (int j = 0; j < 2; ++j) {
 #pragma unroll
                 for (int u = 0; u < 4; ++u) {
-                    const u32x4 unit = unit_of(x, r, u);
+                    const u32x4 unit = unit_of(w, wn * 64 + j * 32 + r32, u);
+                    fw[j][2 * u] = to_f16<0>(unit);
+                    fw[j][2 * u + 1] = to_f16<1>(unit);
+                }
+            }
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                f32x16 part[2] = {};
+#pragma unroll
+                for (int u = 0; u < 4; ++u) {
+                    const u32x4 unit = unit_of(x, wm * 32 * MI + i * 32 + r32, u);
                     const f16x8 a = to_f16<0>(unit), b = to_f16<1>(unit);
                     part[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fw[0][2 * u], a, part[0], 0, 0, 0);
                     part[1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fw[1][2 * u], a, part[1], 0, 0, 0);
                     part[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fw[0][2 * u + 1], b, part[0], 0, 0, 0);
                     part[1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fw[1][2 * u + 1], b, part[1], 0, 0, 0);
                 }
-            } else {
-                i32x8 cx[2];
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const u32x4 unit = unit_of(x, r, u);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) cx[u >> 1][(u & 1) * 4 + k] = (int)unit[k];
-                }
-#pragma unroll
-                for (int j = 0; j < 2; ++j)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        part[j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(cw[j][h], cx[h], part[j], 0, 0, 0, 0, 0, 0);
+                float scale[2];
+                scales_of(from, i, scale);
+                add(acc[i][0], part[0], scale[0]);
+                add(acc[i][1], part[1], scale[1]);
             }
-            const float scale[2] = {s[r] * s[BM + (SWIGLU ? 0 : wn >> 1)], s[r] * s[BM + (SWIGLU ? 1 : wn >> 1)]};
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-#pragma unroll
-                for (int e = 0; e < 16; ++e) acc[i][j][e] = __builtin_fmaf(part[j][e], scale[j], acc[i][j][e]);
-            if constexpr (!SWIGLU) __builtin_amdgcn_sched_barrier(0);  // 3 % against free order
+        };
+        // one block of channels: start the next one's loads and multiply
+        auto step = [&](const u32x4 *now, u32x4 *next, int b) {
+            if (b + 1 < blocks) load(next, b + 1);
+            if (busy) multiply(now);
+            end_step();
+        };
+        for (int b = 0; b < blocks; b += 2) {
+            step(s_0, s_1, b);
+            if (b + 1 < blocks) step(s_1, s_0, b + 1);
         }
-    };
-    // one block of channels: start the next one's loads and multiply
-    auto step = [&](const u32x4 *now, u32x4 *next, int b) {
-        if (b + 1 < blocks) load(next, b + 1);
-        if (busy) multiply(now);
-        end_step();
-    };
-    load(s_0, 0);
-    end_step();
-    for (int b = 0; b < blocks; b += 2) {
-        step(s_0, s_1, b);
-        if (b + 1 < blocks) step(s_1, s_0, b + 1);
+    } else {
+        static_assert(MI % 2 == 0, "rows alternate between two sets of registers");
+        i32x8 cw[2][2], cx[2][2];  // codes of the weights; of the rows in hand and of the next
+        f32x16 part[2];
+        float scale[2];
+        auto read = [&](const u32x4 *rows, i32x8 (&to)[2]) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+                to[h] = codes(rows[r32 * kUnits + (unit0 ^ (4 * h))], rows[r32 * kUnits + (unit0 ^ (4 * h + 2))]);
+        };
+        auto read_rows = [&](const u32x4 *from, int i) {
+            read(from + kX + (wm * MI + i) * 32 * kUnits, cx[i & 1]);
+            float both[2];
+            scales_of(from, i, both);
+            scale[i & 1] = both[0];
+        };
+        auto product = [&](int i, int j) {
+            const f32x16 zero = {};
+            part[j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(cw[j][0], cx[i & 1][0], zero, 0, 0, 0, 0, 0, 0);
+            part[j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(cw[j][1], cx[i & 1][1], part[j], 0, 0, 0, 0, 0, 0);
+        };
+        // A block of channels is MI times 32 rows by 2 times 32 weight rows.  While one product runs the
+        // one before it is scaled and added and the next rows are read; the last rows' products come
+        // behind the barrier, so that they hide the first reads of the next block.
+        float keep = 0.0f;  // scale of part[1], which is added behind the next product
+        part[1] = f32x16{};
+        auto step = [&](u32x4 *now, const u32x4 *next, int b) {
+#pragma unroll
+            for (int i = 0; i < MI; ++i) {
+                if (i + 1 < MI) {
+                    if (busy) read_rows(now, i + 1);
+                } else {
+                    end_step();
+                    if (b + 2 < blocks) load(now, b + 2);
+                    if (busy) read_rows(next, 0);
+                }
+                if (busy) {
+                    __builtin_amdgcn_sched_barrier(0);
+                    product(i, 0);
+                    __builtin_amdgcn_sched_barrier(0);
+                    add(acc[(i + MI - 1) % MI][1], part[1], keep);
+                    if (i + 1 == MI) read(next + kW + wn * 64 * kUnits, cw[0]);
+                    __builtin_amdgcn_sched_barrier(0);
+                    product(i, 1);
+                    __builtin_amdgcn_sched_barrier(0);
+                    keep = scale[i & 1];
+                    add(acc[i][0], part[0], keep);
+                    if (i + 1 == MI) read(next + kW + (wn * 64 + 32) * kUnits, cw[1]);
+                    __builtin_amdgcn_sched_barrier(0);
+                }
+            }
+        };
+        if (blocks > 1) load(s_1, 1);
+        if (busy) {
+            read_rows(s_0, 0);
+            read(s_0 + kW + wn * 64 * kUnits, cw[0]);
+            read(s_0 + kW + (wn * 64 + 32) * kUnits, cw[1]);
+        }
+        for (int b = 0; b < blocks; b += 2) {
+            step(s_0, s_1, b);
+            if (b + 1 < blocks) step(s_1, s_0, b + 1);
+        }
+        add(acc[MI - 1][1], part[1], keep);
     }
 
-    // the lane's element e of a 32 x 32 result: row r32, weight row 8 (e / 4) + 4 half + e % 4
+    // The lane's element e of a 32 x 32 result: row r32, weight row 8 (e / 4) + 4 half + e % 4.  A
+    // direct store would put 16 bytes into each of 32 rows; results go through LDS instead and out as
+    // whole rows (32768 rows x 7168, 2048 channels: 731 -> 675 us, and 657 past the caches).
     if constexpr (!SWIGLU) {
-        uint16_t *out = static_cast<uint16_t *>(p.out);
+        // the rows of each half of the block in a buffer of their own, 512 bytes a row, 16-byte units
+        // rotated by the row
+        static_assert(32 * MI * kBN * 2 <= kBuffer * 16, "half the block's rows fit a buffer");
+        end_step();
+        u32x4 *rows = wm == 0 ? s_0 : s_1;
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
-            const int r = wm * 32 * MI + i * 32 + r32;
-            if (r >= t.rows) continue;
+            const int r = i * 32 + r32;
 #pragma unroll
             for (int j = 0; j < 2; ++j) {
 #pragma unroll
                 for (int g = 0; g < 4; ++g) {
-                    const int c = col_tile * kBN + wn * 64 + j * 32 + g * 8 + half * 4;
-                    if (c >= p.n) continue;  // n is a multiple of 8: all four or none
                     uint2 o;
                     o.x = pack_bf16(acc[i][j][4 * g], acc[i][j][4 * g + 1]);
                     o.y = pack_bf16(acc[i][j][4 * g + 2], acc[i][j][4 * g + 3]);
-                    *reinterpret_cast<uint2 *>(out + (t.first + r) * p.n + c) = o;
+                    reinterpret_cast<uint2 *>(rows + r * 32 + ((wn * 8 + j * 4 + g) ^ r32))[half] = o;
                 }
             }
+        }
+        __syncthreads();
+        uint16_t *out = static_cast<uint16_t *>(p.out);
+        const int unit = lane & 31, c = col_tile * kBN + unit * 8;
+        for (int r = wn * 2 + (lane >> 5); r < 32 * MI; r += 2 * WN) {
+            const int row = wm * 32 * MI + r;
+            if (row >= t.rows || c >= p.n) continue;  // n is a multiple of 8: all eight or none
+            __builtin_nontemporal_store(rows[r * 32 + (unit ^ (r & 31))],
+                                        reinterpret_cast<u32x4 *>(out + (t.first + row) * p.n + c));
         }
     } else {
         float *s_top = reinterpret_cast<float *>(s_0);  // [WN][BM]: the tiles are done with
@@ -322,37 +383,48 @@ __global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(Gemm
             if (half == 0) s_top[wn * BM + wm * 32 * MI + i * 32 + r32] = top;
         }
         __syncthreads();
-        uint8_t *out = static_cast<uint8_t *>(p.out);
+        uint32_t *codes = reinterpret_cast<uint32_t *>(s_1);  // [BM][32] words, 16-byte units rotated by the row
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
             const int r = wm * 32 * MI + i * 32 + r32;
-            if (r >= t.rows) continue;
             float m = kE4m3AmaxFloor;
 #pragma unroll
             for (int j = 0; j < WN; ++j) m = fmaxf(m, s_top[j * BM + r]);
             const float inv = kE4m3Max / m;
-            if (wn == 0 && half == 0) p.out_scales[(t.first + r) * (p.n / kScaleBlock) + col_tile] = m / kE4m3Max;
+            if (wn == 0 && half == 0 && r < t.rows)
+                p.out_scales[(t.first + r) * (p.n / kScaleBlock) + col_tile] = m / kE4m3Max;
 #pragma unroll
             for (int g = 0; g < 4; ++g) {
-                const int c = col_tile * 128 + wn * HALF + g * 8 + half * 4;
-                *reinterpret_cast<uint32_t *>(out + (t.first + r) * p.n + c) =
+                const int word = wn * 8 + g * 2 + half;
+                codes[r * 32 + ((word >> 2) ^ (r & 7)) * 4 + (word & 3)] =
                     e4m3_pack4(acc[i][0][4 * g] * inv, acc[i][0][4 * g + 1] * inv, acc[i][0][4 * g + 2] * inv,
                                acc[i][0][4 * g + 3] * inv);
             }
         }
+        __syncthreads();
+        uint8_t *out = static_cast<uint8_t *>(p.out);
+        for (int i = threadIdx.x; i < BM * kUnits; i += kBlockThreads) {
+            const int r = i / kUnits, unit = i % kUnits;
+            if (r >= t.rows) continue;
+            *reinterpret_cast<u32x4 *>(out + (t.first + r) * p.n + col_tile * 128 + unit * 16) =
+                s_1[r * kUnits + (unit ^ (r & 7))];
+        }
     }
 }
 
-// Few rows: 16 MF rows x 64 NG weight rows a block of NG x KS waves.  The weights are read once and
-// by one wave only, so they go straight to registers: no LDS, no barrier, and every wave has the
-// next block of channels on its way while it multiplies one.  The KS waves of a group take every
-// KS-th block of channels and add up through LDS at the end.
-template <bool SWIGLU, int MF, int NG, int KS, int WAVES>
-__global__ __launch_bounds__(NG *KS *kWave, WAVES) void expert_gemm_narrow_kernel(GemmArgs p, int col_tiles) {
+// Few rows: 16 rows x 64 NG weight rows a block of NG x KS waves.  The weights are read once and by
+// one wave only, so they go straight to registers: no LDS, no barrier, and every wave has the next
+// block of channels on its way while it multiplies one.  The KS waves of a group take every KS-th
+// block of channels and add up through LDS at the end.  Bound by the weights' bytes: 128 rows of 32
+// experts take 175 us for 0.94 GB (SwiGLU) and 82-85 us for 0.47 GB, 5.4 to 5.7 TB/s.  Three waves a
+// SIMD hold all they keep in registers; four spill, and 8-wave blocks wait longer at their end
+// (97-100 us for the second).
+template <bool SWIGLU, int NG, int KS>
+__global__ __launch_bounds__(NG *KS *kWave, 3) void expert_gemm_narrow_kernel(GemmArgs p, int col_tiles) {
     static_assert(!SWIGLU || NG == 4, "a block holds a scale's 128 outputs");
-    constexpr int BM = 16 * MF, BN = 64 * NG;
+    constexpr int BM = 16, BN = 64 * NG;
     constexpr int OWN = (SWIGLU ? 2 : 4) / KS;  // 16-column results of its group that a wave finishes
-    __shared__ f32x4 s_sum[NG][KS][4][MF][kWave];
+    __shared__ f32x4 s_sum[NG][KS][4][kWave];
     __shared__ float s_top[NG * KS][BM];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -367,14 +439,17 @@ __global__ __launch_bounds__(NG *KS *kWave, WAVES) void expert_gemm_narrow_kerne
     const __amdgpu_buffer_rsrc_t wbuf = descriptor(p.w + (int64_t)t.expert * wrows * p.k, (uint32_t)wrows * p.k);
     const __amdgpu_buffer_rsrc_t sbuf = descriptor(p.x_scales + t.first * blocks, (uint32_t)t.rows * blocks * 4);
 
+    // rows past the segment and weight rows past the last are past the descriptors' ends: they read
+    // as 0 and are not stored
     const int q = lane >> 4, r16 = lane & 15;
+    const int xat = r16 * p.k + q * 16, sat = r16 * blocks * 4;
     // column (output) of the group's first weight row; SWIGLU: rows 0-31 are gate rows, 32-63 the up rows of the same
     const int c0 = SWIGLU ? col_tile * 128 + group * 32 : col_tile * BN + group * 64;
     int wat[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int row = SWIGLU ? (j < 2 ? c0 + j * 16 : p.n + c0 + (j - 2) * 16) : c0 + j * 16;
-        wat[j] = (row + r16) * p.k + q * 16;  // rows past the last are past the descriptor's end and read as 0
+        wat[j] = (row + r16) * p.k + q * 16;
     }
     const float *sw0 = p.w_scales + (int64_t)t.expert * scale_rows * blocks;
     const float *sw1;
@@ -387,8 +462,8 @@ __global__ __launch_bounds__(NG *KS *kWave, WAVES) void expert_gemm_narrow_kerne
     }
 
     struct Codes {
-        u32x4 w[4][2], x[MF][2];
-        float sx[MF], sw[2];
+        u32x4 w[4][2], x[2];
+        float sx, sw[2];
     };
     auto load = [&](Codes &c, int b) {
 #pragma unroll
@@ -396,58 +471,40 @@ __global__ __launch_bounds__(NG *KS *kWave, WAVES) void expert_gemm_narrow_kerne
             c.w[j][0] = __builtin_amdgcn_raw_buffer_load_b128(wbuf, wat[j], b * kScaleBlock, 0);
             c.w[j][1] = __builtin_amdgcn_raw_buffer_load_b128(wbuf, wat[j] + 64, b * kScaleBlock, 0);
         }
-#pragma unroll
-        for (int i = 0; i < MF; ++i) {
-            const int at = (i * 16 + r16) * p.k + q * 16;
-            c.x[i][0] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, at, b * kScaleBlock, 0);
-            c.x[i][1] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, at + 64, b * kScaleBlock, 0);
-            c.sx[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sbuf, (i * 16 + r16) * blocks * 4, b * 4, 0));
-        }
+        c.x[0] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, xat, b * kScaleBlock, 0);
+        c.x[1] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, xat + 64, b * kScaleBlock, 0);
+        c.sx = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sbuf, sat, b * 4, 0));
         c.sw[0] = sw0[b];
         c.sw[1] = SWIGLU ? sw1[b] : c.sw[0];
     };
-    f32x4 acc[MF][4];
+    f32x4 acc[4];
 #pragma unroll
-    for (int i = 0; i < MF; ++i)
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
     auto multiply = [&](const Codes &c) {
-        f16x8 fx[MF][4];
+        f16x8 fx[4];
         if constexpr (SWIGLU) {
 #pragma unroll
-            for (int i = 0; i < MF; ++i)
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    fx[i][2 * h] = to_f16<0>(c.x[i][h]);
-                    fx[i][2 * h + 1] = to_f16<1>(c.x[i][h]);
-                }
+            for (int h = 0; h < 2; ++h) {
+                fx[2 * h] = to_f16<0>(c.x[h]);
+                fx[2 * h + 1] = to_f16<1>(c.x[h]);
+            }
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            f16x8 fw[4];
+            f32x4 part = {0.f, 0.f, 0.f, 0.f};
             if constexpr (SWIGLU) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    fw[2 * h] = to_f16<0>(c.w[j][h]);
-                    fw[2 * h + 1] = to_f16<1>(c.w[j][h]);
+                    part = __builtin_amdgcn_mfma_f32_16x16x32_f16(to_f16<0>(c.w[j][h]), fx[2 * h], part, 0, 0, 0);
+                    part = __builtin_amdgcn_mfma_f32_16x16x32_f16(to_f16<1>(c.w[j][h]), fx[2 * h + 1], part, 0, 0, 0);
                 }
+            } else {
+                part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(codes(c.w[j][0], c.w[j][1]), codes(c.x[0], c.x[1]),
+                                                                        part, 0, 0, 0, 0, 0, 0);
             }
+            const float s = c.sx * c.sw[j >> 1];
 #pragma unroll
-            for (int i = 0; i < MF; ++i) {
-                f32x4 part = {0.f, 0.f, 0.f, 0.f};
-                if constexpr (SWIGLU) {
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        part = __builtin_amdgcn_mfma_f32_16x16x32_f16(fw[k], fx[i][k], part, 0, 0, 0);
-                } else {
-                    part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(codes(c.w[j][0], c.w[j][1]),
-                                                                            codes(c.x[i][0], c.x[i][1]), part, 0, 0, 0,
-                                                                            0, 0, 0);
-                }
-                const float s = c.sx[i] * c.sw[j >> 1];
-#pragma unroll
-                for (int k = 0; k < 4; ++k) acc[i][j][k] = __builtin_fmaf(part[k], s, acc[i][j][k]);
-            }
+            for (int k = 0; k < 4; ++k) acc[j][k] = __builtin_fmaf(part[k], s, acc[j][k]);
         }
     };
     Codes even, odd;
@@ -461,66 +518,53 @@ __global__ __launch_bounds__(NG *KS *kWave, WAVES) void expert_gemm_narrow_kerne
 
     // the KS sums of each 16 x 16 result, added in order by the wave that finishes it
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int i = 0; i < MF; ++i) s_sum[group][ks][j][i][lane] = acc[i][j];
+    for (int j = 0; j < 4; ++j) s_sum[group][ks][j][lane] = acc[j];
     __syncthreads();
-    auto total = [&](int j, int i) {
-        f32x4 v = s_sum[group][0][j][i][lane];
+    auto total = [&](int j) {
+        f32x4 v = s_sum[group][0][j][lane];
 #pragma unroll
-        for (int k = 1; k < KS; ++k) v += s_sum[group][k][j][i][lane];
+        for (int k = 1; k < KS; ++k) v += s_sum[group][k][j][lane];
         return v;
     };
+    const bool inside = r16 < t.rows;
     if constexpr (!SWIGLU) {
-        uint16_t *out = static_cast<uint16_t *>(p.out);
+        uint16_t *out = static_cast<uint16_t *>(p.out) + (t.first + r16) * p.n;
 #pragma unroll
-        for (int i = 0; i < MF; ++i) {
-            const int r = i * 16 + r16;
-#pragma unroll
-            for (int o = 0; o < OWN; ++o) {
-                const int j = ks * OWN + o, c = c0 + j * 16 + q * 4;
-                const f32x4 v = total(j, i);
-                if (r >= t.rows || c >= p.n) continue;  // n is a multiple of 8: all four or none
-                uint2 pair;
-                pair.x = pack_bf16(v[0], v[1]);
-                pair.y = pack_bf16(v[2], v[3]);
-                *reinterpret_cast<uint2 *>(out + (t.first + r) * p.n + c) = pair;
-            }
+        for (int o = 0; o < OWN; ++o) {
+            const int j = ks * OWN + o, c = c0 + j * 16 + q * 4;
+            const f32x4 v = total(j);
+            uint2 pair;
+            pair.x = pack_bf16(v[0], v[1]);
+            pair.y = pack_bf16(v[2], v[3]);
+            if (inside && c < p.n) *reinterpret_cast<uint2 *>(out + c) = pair;  // n is a multiple of 8: all four or none
         }
     } else {
-        f32x4 a[MF][OWN];
+        f32x4 a[OWN];
+        float top = 0.0f;
 #pragma unroll
-        for (int i = 0; i < MF; ++i) {
-            float top = 0.0f;
+        for (int o = 0; o < OWN; ++o) {
+            const f32x4 g = total(ks * OWN + o), u = total(2 + ks * OWN + o);
 #pragma unroll
-            for (int o = 0; o < OWN; ++o) {
-                const f32x4 g = total(ks * OWN + o, i), u = total(2 + ks * OWN + o, i);
-#pragma unroll
-                for (int k = 0; k < 4; ++k) {
-                    a[i][o][k] = g[k] / (1.0f + expf(-g[k])) * u[k];
-                    top = fmaxf(top, fabsf(a[i][o][k]));
-                }
+            for (int k = 0; k < 4; ++k) {
+                a[o][k] = g[k] / (1.0f + expf(-g[k])) * u[k];
+                top = fmaxf(top, fabsf(a[o][k]));
             }
-            top = fmaxf(top, __shfl_xor(top, 16));
-            top = fmaxf(top, __shfl_xor(top, 32));
-            if (q == 0) s_top[wave][i * 16 + r16] = top;
         }
+        top = fmaxf(top, __shfl_xor(top, 16));
+        top = fmaxf(top, __shfl_xor(top, 32));
+        if (q == 0) s_top[wave][r16] = top;
         __syncthreads();
-        uint8_t *out = static_cast<uint8_t *>(p.out);
+        float m = kE4m3AmaxFloor;
 #pragma unroll
-        for (int i = 0; i < MF; ++i) {
-            const int r = i * 16 + r16;
-            if (r >= t.rows) continue;
-            float m = kE4m3AmaxFloor;
+        for (int j = 0; j < NG * KS; ++j) m = fmaxf(m, s_top[j][r16]);
+        const float inv = kE4m3Max / m;
+        if (!inside) return;
+        if (wave == 0 && q == 0) p.out_scales[(t.first + r16) * (p.n / kScaleBlock) + col_tile] = m / kE4m3Max;
+        uint8_t *out = static_cast<uint8_t *>(p.out) + (t.first + r16) * p.n + c0 + ks * OWN * 16 + q * 4;
 #pragma unroll
-            for (int j = 0; j < NG * KS; ++j) m = fmaxf(m, s_top[j][r]);
-            const float inv = kE4m3Max / m;
-            if (wave == 0 && q == 0) p.out_scales[(t.first + r) * (p.n / kScaleBlock) + col_tile] = m / kE4m3Max;
-#pragma unroll
-            for (int o = 0; o < OWN; ++o)
-                *reinterpret_cast<uint32_t *>(out + (t.first + r) * p.n + c0 + (ks * OWN + o) * 16 + q * 4) =
-                    e4m3_pack4(a[i][o][0] * inv, a[i][o][1] * inv, a[i][o][2] * inv, a[i][o][3] * inv);
-        }
+        for (int o = 0; o < OWN; ++o)
+            *reinterpret_cast<uint32_t *>(out + o * 16) =
+                e4m3_pack4(a[o][0] * inv, a[o][1] * inv, a[o][2] * inv, a[o][3] * inv);
     }
 }
 
@@ -536,20 +580,23 @@ struct Plan {
     int threads, rows, cols;
 };
 
-template <bool SWIGLU, int MF, int NG, int KS, int WAVES>
-Plan narrow() {
-    return {expert_gemm_narrow_kernel<SWIGLU, MF, NG, KS, WAVES>, NG * KS * kWave, 16 * MF, SWIGLU ? 128 : 64 * NG};
-}
-
+// By the mean rows of an expert (all that the host knows of the sizes).  Measured over 32 experts, SwiGLU
+// of 7168 channels to 2048 and product of 2048 to 7168:
+//   mean rows            4    8   12   16   32   64   96  128  192  256  512
+//   SwiGLU   narrow    177  179  239  236  360                              us
+//            wide 128  186  187  189  190  194  216  251  408  503  607 1092
+//   product  narrow     85   90  100  114  176                              us
+//            wide 128  103  104  106  105  109  115  119  156  187  233  396
+//            wide 256                           122  125  137  155  195  335
+// Up to 8 rows the narrow kernel leads; 128 rows a block serve until experts fill more than one.
 Plan plan(const GemmArgs &a) {
     const int mean = a.num_rows / a.num_experts;
     if (a.swiglu) {
-        if (mean <= 8) return narrow<true, 1, 4, 1, 3>();
-        if (mean <= 32) return narrow<true, 2, 4, 1, 2>();
+        if (mean <= 8) return {expert_gemm_narrow_kernel<true, 4, 1>, 4 * kWave, 16, 128};
         return {expert_gemm_wide_kernel<true, 2>, kBlockThreads, 128, 128};
     }
-    if (mean <= 8) return narrow<false, 1, 2, 2, 3>();
-    if (mean <= 32) return narrow<false, 2, 2, 2, 2>();
+    if (mean <= 8) return {expert_gemm_narrow_kernel<false, 2, 2>, 4 * kWave, 16, 128};
+    if (mean <= 112) return {expert_gemm_wide_kernel<false, 2>, kBlockThreads, 128, kBN};
     return {expert_gemm_wide_kernel<false, 4>, kBlockThreads, 256, kBN};
 }
 

@@ -102,7 +102,7 @@ def test_product_many_experts(rows, E):
     assert status == 0
 
 
-@pytest.mark.parametrize("mean", [1, 8, 9, 32, 33, 128, 300])
+@pytest.mark.parametrize("mean", [1, 8, 9, 64, 112, 113, 300])
 @pytest.mark.parametrize("exact", [True, False])
 def test_rows_an_expert_on_both_sides_of_each_choice_of_kernel(mean, exact):
     """Both outputs at mean segment sizes around those where another kernel takes over, uneven around the mean."""
