@@ -122,10 +122,15 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t src, float *d
                                              0, 0);
 }
 
-// Ends a step: the wave's loads into LDS have landed and its reads are over, and then every wave's.
+// Ends a step: the wave's reads of LDS are over and no more than `left` (0 .. 15) of its loads are
+// under way (they end in order), and then every wave's.  __syncthreads would wait for all loads.
+template <int left>
 __device__ __forceinline__ void end_step() {
-    __builtin_amdgcn_s_waitcnt(0x0070);  // vmcnt(0), lgkmcnt(0)
-    __syncthreads();
+    static_assert(left >= 0 && left < 16, "the low bits of vmcnt");
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0070 | left);  // vmcnt(left), lgkmcnt(0)
+    __builtin_amdgcn_s_barrier();
+    asm volatile("" ::: "memory");
 }
 
 // Unit of row r that lies at place c of its row in LDS (and the place of unit c).  A 16-byte read
@@ -141,13 +146,15 @@ __global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(Gemm
     constexpr int WM = 2, WN = 4, BM = 32 * MI * WM, HALF = 32;
     static_assert(2 * HALF * WN == kBN, "256 weight rows a block");
     constexpr int XL = BM * kUnits / kBlockThreads, WL = kBN * kUnits / kBlockThreads;  // units a thread loads
-    // Two buffers: while one block of channels is multiplied the next is on its way.  A wave's last
-    // load of a step is of scales: rows' by the first BM lanes, the weights' two by the lanes of the
-    // next wave (the others repeat those).  (One array a buffer: the compiler tells them apart, and
-    // would wait for all loads before a read of an array that it does not.)
+    // STAGES buffers: while one block of channels is multiplied the next ones are on their way.  A
+    // wave's last load of a step is of scales: rows' by the first BM lanes, the weights' two by the
+    // lanes of the next wave (the others repeat those).  (One array a buffer: the compiler tells them
+    // apart, and would wait for all loads before a read of an array that it does not.)
+    constexpr int STAGES = MI == 2 ? 3 : 2;
+    constexpr int kLoads = XL + WL + 1;  // of a wave and step
     static_assert(BM <= 64 * (WM * WN - 1), "a wave is left for the weights' scales");
     constexpr int kX = 0, kW = BM * kUnits, kS = kW + kBN * kUnits, kBuffer = kS + kBlockThreads / 4;
-    __shared__ u32x4 s_0[kBuffer], s_1[kBuffer];
+    __shared__ u32x4 s_0[kBuffer], s_1[kBuffer], s_2[STAGES == 3 ? kBuffer : 1];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
@@ -200,17 +207,20 @@ __global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(Gemm
 
     const int half = lane >> 5, r32 = lane & 31;
     const bool busy = wm * 32 * MI < t.rows;  // the other half of a part tile has nothing to multiply
+    // Past the last block the loads go on, from behind the descriptors' ends (they fetch nothing):
+    // that every step issues the same number is what lets the waits count.
     auto load = [&](u32x4 *to, int b) {
+        const int past = b < blocks ? 0 : INT_MIN, from = b < blocks ? b : 0;
         int xat = x_first, wat = w_first;
-        asm volatile("" : "+v"(xat), "+v"(wat));  // as in multiply()
+        asm volatile("" : "+v"(xat), "+v"(wat));  // addresses are cheaper formed anew than kept in registers
 #pragma unroll
         for (int i = 0; i < XL; ++i)
-            load_to_lds(xbuf, to + kX + i * kBlockThreads + wave * kWave, xat + i * kStep * p.k, b * kScaleBlock);
+            load_to_lds(xbuf, to + kX + i * kBlockThreads + wave * kWave, xat + (i * kStep * p.k + past), from * kScaleBlock);
 #pragma unroll
         for (int i = 0; i < WL; ++i)
-            load_to_lds(wbuf, to + kW + i * kBlockThreads + wave * kWave, wat + i * (SWIGLU ? kStep / 2 : kStep) * p.k,
-                        b * kScaleBlock);
-        load_to_lds(sbuf, reinterpret_cast<float *>(to + kS) + wave * kWave, sat, b * 4);
+            load_to_lds(wbuf, to + kW + i * kBlockThreads + wave * kWave,
+                        wat + (i * (SWIGLU ? kStep / 2 : kStep) * p.k + past), from * kScaleBlock);
+        load_to_lds(sbuf, reinterpret_cast<float *>(to + kS) + wave * kWave, sat + past, from * 4);
     };
     // the lane's units of any row it reads: 2 u + half, where the rotation has put them
     const int unit0 = rotate(r32, half);
@@ -225,8 +235,10 @@ __global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(Gemm
         for (int e = 0; e < 16; ++e) sum[e] = __builtin_fmaf(part[e], scale, sum[e]);
     };
     load(s_0, 0);
-    end_step();
+    load(s_1, 1);
     if constexpr (SWIGLU) {
+        static_assert(STAGES == 3, "a block is loaded two steps ahead");
+        end_step<kLoads>();
         auto multiply = [&](const u32x4 *from) {
             const u32x4 *x = from + kX, *w = from + kW;
             int u0 = unit0;
@@ -260,15 +272,16 @@ __global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(Gemm
                 add(acc[i][1], part[1], scale[1]);
             }
         };
-        // one block of channels: start the next one's loads and multiply
-        auto step = [&](const u32x4 *now, u32x4 *next, int b) {
-            if (b + 1 < blocks) load(next, b + 1);
+        // one block of channels: start the loads of the second next, multiply, let the next one's land
+        auto step = [&](const u32x4 *now, u32x4 *later, int b) {
+            load(later, b + 2);
             if (busy) multiply(now);
-            end_step();
+            end_step<kLoads>();
         };
-        for (int b = 0; b < blocks; b += 2) {
-            step(s_0, s_1, b);
+        for (int b = 0; b < blocks; b += 3) {
+            step(s_0, s_2, b);
             if (b + 1 < blocks) step(s_1, s_0, b + 1);
+            if (b + 2 < blocks) step(s_2, s_1, b + 2);
         }
     } else {
         static_assert(MI % 2 == 0, "rows alternate between two sets of registers");
@@ -302,8 +315,8 @@ __global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(Gemm
                 if (i + 1 < MI) {
                     if (busy) read_rows(now, i + 1);
                 } else {
-                    end_step();
-                    if (b + 2 < blocks) load(now, b + 2);
+                    end_step<(STAGES - 2) * kLoads>();
+                    load(now, b + STAGES);
                     if (busy) read_rows(next, 0);
                 }
                 if (busy) {
@@ -322,15 +335,18 @@ __global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(Gemm
                 }
             }
         };
-        if (blocks > 1) load(s_1, 1);
+        if constexpr (STAGES == 3) load(s_2, 2);
+        end_step<(STAGES - 1) * kLoads>();
         if (busy) {
             read_rows(s_0, 0);
             read(s_0 + kW + wn * 64 * kUnits, cw[0]);
             read(s_0 + kW + (wn * 64 + 32) * kUnits, cw[1]);
         }
-        for (int b = 0; b < blocks; b += 2) {
+        for (int b = 0; b < blocks; b += STAGES) {
             step(s_0, s_1, b);
-            if (b + 1 < blocks) step(s_1, s_0, b + 1);
+            if (b + 1 < blocks) step(s_1, STAGES == 3 ? s_2 : s_0, b + 1);
+            if constexpr (STAGES == 3)
+                if (b + 2 < blocks) step(s_2, s_0, b + 2);
         }
         add(acc[MI - 1][1], part[1], keep);
     }
@@ -338,11 +354,11 @@ __global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(Gemm
     // The lane's element e of a 32 x 32 result: row r32, weight row 8 (e / 4) + 4 half + e % 4.  A
     // direct store would put 16 bytes into each of 32 rows; results go through LDS instead and out as
     // whole rows (32768 rows x 7168, 2048 channels: 731 -> 675 us, and 657 past the caches).
+    end_step<0>();  // nothing reads the buffers or writes to them any more
     if constexpr (!SWIGLU) {
         // the rows of each half of the block in a buffer of their own, 512 bytes a row, 16-byte units
         // rotated by the row
         static_assert(32 * MI * kBN * 2 <= kBuffer * 16, "half the block's rows fit a buffer");
-        end_step();
         u32x4 *rows = wm == 0 ? s_0 : s_1;
 #pragma unroll
         for (int i = 0; i < MI; ++i) {
@@ -412,20 +428,24 @@ __global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(Gemm
     }
 }
 
-// Few rows: 16 rows x 64 NG weight rows a block of NG x KS waves.  The weights are read once and by
-// one wave only, so they go straight to registers: no LDS, no barrier, and every wave has the next
-// block of channels on its way while it multiplies one.  The KS waves of a group take every KS-th
-// block of channels and add up through LDS at the end.  Bound by the weights' bytes: 128 rows of 32
-// experts take 175 us for 0.94 GB (SwiGLU) and 82-85 us for 0.47 GB, 5.4 to 5.7 TB/s.  Three waves a
-// SIMD hold all they keep in registers; four spill, and 8-wave blocks wait longer at their end
-// (97-100 us for the second).
-template <bool SWIGLU, int NG, int KS>
-__global__ __launch_bounds__(NG *KS *kWave, 3) void expert_gemm_narrow_kernel(GemmArgs p, int col_tiles) {
+// Few rows: 16 MF rows x 64 NG weight rows a block of NG x KS waves, WAVES of them a SIMD.  Each wave
+// reads weights of its own, once, so they go straight to registers: no LDS, no barrier, and every
+// wave has the next block of channels on its way while it multiplies one.  The KS waves of a group
+// take every KS-th block of channels and add up through LDS at the end.
+//
+// With rows for many experts this is bound by the weights' bytes: 128 rows of 32 experts take 175 us
+// for 0.94 GB (SwiGLU) and 82-85 us for 0.47 GB, 5.4 to 5.7 TB/s.  (Three waves a SIMD hold all they
+// keep in registers; four spill, and 8-wave blocks wait longer at their end: 97-100 us for the
+// second.)  Neighbouring lanes read different rows, 16 bytes each, which one compute unit takes at 16
+// bytes a clock -- enough for all of them together, little for a few blocks alone.  There the waves of
+// a block share the channels eight ways: 16 rows x 2048 of 7168 channels 44 -> 22 us.
+template <bool SWIGLU, int MF, int NG, int KS, int WAVES>
+__global__ __launch_bounds__(NG *KS *kWave, WAVES) void expert_gemm_narrow_kernel(GemmArgs p, int col_tiles) {
     static_assert(!SWIGLU || NG == 4, "a block holds a scale's 128 outputs");
-    constexpr int BM = 16, BN = 64 * NG;
-    constexpr int OWN = (SWIGLU ? 2 : 4) / KS;  // 16-column results of its group that a wave finishes
-    __shared__ f32x4 s_sum[NG][KS][4][kWave];
-    __shared__ float s_top[NG * KS][BM];
+    constexpr int BM = 16 * MF, BN = 64 * NG;
+    constexpr int SETS = SWIGLU ? 2 : 4;  // 16 columns of output each, of a group
+    __shared__ f32x4 s_sum[NG][KS][4][MF][kWave];
+    __shared__ float s_top[NG][SETS][BM];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int group = wave % NG, ks = wave / NG;
@@ -462,8 +482,8 @@ __global__ __launch_bounds__(NG *KS *kWave, 3) void expert_gemm_narrow_kernel(Ge
     }
 
     struct Codes {
-        u32x4 w[4][2], x[2];
-        float sx, sw[2];
+        u32x4 w[4][2], x[MF][2];
+        float sx[MF], sw[2];
     };
     auto load = [&](Codes &c, int b) {
 #pragma unroll
@@ -471,40 +491,48 @@ __global__ __launch_bounds__(NG *KS *kWave, 3) void expert_gemm_narrow_kernel(Ge
             c.w[j][0] = __builtin_amdgcn_raw_buffer_load_b128(wbuf, wat[j], b * kScaleBlock, 0);
             c.w[j][1] = __builtin_amdgcn_raw_buffer_load_b128(wbuf, wat[j] + 64, b * kScaleBlock, 0);
         }
-        c.x[0] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, xat, b * kScaleBlock, 0);
-        c.x[1] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, xat + 64, b * kScaleBlock, 0);
-        c.sx = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sbuf, sat, b * 4, 0));
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+            c.x[i][0] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, xat + i * 16 * p.k, b * kScaleBlock, 0);
+            c.x[i][1] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, xat + i * 16 * p.k + 64, b * kScaleBlock, 0);
+            c.sx[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sbuf, sat + i * 16 * blocks * 4, b * 4, 0));
+        }
         c.sw[0] = sw0[b];
         c.sw[1] = SWIGLU ? sw1[b] : c.sw[0];
     };
-    f32x4 acc[4];
+    f32x4 acc[MF][4];
 #pragma unroll
-    for (int j = 0; j < 4; ++j) acc[j] = f32x4{0.f, 0.f, 0.f, 0.f};
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     auto multiply = [&](const Codes &c) {
-        f16x8 fx[4];
-        if constexpr (SWIGLU) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                fx[2 * h] = to_f16<0>(c.x[h]);
-                fx[2 * h + 1] = to_f16<1>(c.x[h]);
-            }
-        }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
-            f32x4 part = {0.f, 0.f, 0.f, 0.f};
+            f16x8 fw[4];
             if constexpr (SWIGLU) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    part = __builtin_amdgcn_mfma_f32_16x16x32_f16(to_f16<0>(c.w[j][h]), fx[2 * h], part, 0, 0, 0);
-                    part = __builtin_amdgcn_mfma_f32_16x16x32_f16(to_f16<1>(c.w[j][h]), fx[2 * h + 1], part, 0, 0, 0);
+                    fw[2 * h] = to_f16<0>(c.w[j][h]);
+                    fw[2 * h + 1] = to_f16<1>(c.w[j][h]);
                 }
-            } else {
-                part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(codes(c.w[j][0], c.w[j][1]), codes(c.x[0], c.x[1]),
-                                                                        part, 0, 0, 0, 0, 0, 0);
             }
-            const float s = c.sx * c.sw[j >> 1];
 #pragma unroll
-            for (int k = 0; k < 4; ++k) acc[j][k] = __builtin_fmaf(part[k], s, acc[j][k]);
+            for (int i = 0; i < MF; ++i) {
+                f32x4 part = {0.f, 0.f, 0.f, 0.f};
+                if constexpr (SWIGLU) {
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        part = __builtin_amdgcn_mfma_f32_16x16x32_f16(fw[2 * h], to_f16<0>(c.x[i][h]), part, 0, 0, 0);
+                        part = __builtin_amdgcn_mfma_f32_16x16x32_f16(fw[2 * h + 1], to_f16<1>(c.x[i][h]), part, 0, 0, 0);
+                    }
+                } else {
+                    part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
+                        codes(c.w[j][0], c.w[j][1]), codes(c.x[i][0], c.x[i][1]), part, 0, 0, 0, 0, 0, 0);
+                }
+                const float s = c.sx[i] * c.sw[j >> 1];
+#pragma unroll
+                for (int k = 0; k < 4; ++k) acc[i][j][k] = __builtin_fmaf(part[k], s, acc[i][j][k]);
+            }
         }
     };
     Codes even, odd;
@@ -516,55 +544,67 @@ __global__ __launch_bounds__(NG *KS *kWave, 3) void expert_gemm_narrow_kernel(Ge
         if (b + KS < blocks) multiply(odd);
     }
 
-    // the KS sums of each 16 x 16 result, added in order by the wave that finishes it
+    // the KS sums of each 16 x 16 result, added in order; the waves of a group share its results out
 #pragma unroll
-    for (int j = 0; j < 4; ++j) s_sum[group][ks][j][lane] = acc[j];
+    for (int i = 0; i < MF; ++i)
+#pragma unroll
+        for (int j = 0; j < 4; ++j) s_sum[group][ks][j][i][lane] = acc[i][j];
     __syncthreads();
-    auto total = [&](int j) {
-        f32x4 v = s_sum[group][0][j][lane];
+    auto total = [&](int j, int i) {
+        f32x4 v = s_sum[group][0][j][i][lane];
 #pragma unroll
-        for (int k = 1; k < KS; ++k) v += s_sum[group][k][j][lane];
+        for (int k = 1; k < KS; ++k) v += s_sum[group][k][j][i][lane];
         return v;
     };
-    const bool inside = r16 < t.rows;
+    constexpr int SHARE = (SETS * MF + KS - 1) / KS;  // results a wave finishes, at most
     if constexpr (!SWIGLU) {
-        uint16_t *out = static_cast<uint16_t *>(p.out) + (t.first + r16) * p.n;
+        uint16_t *out = static_cast<uint16_t *>(p.out);
 #pragma unroll
-        for (int o = 0; o < OWN; ++o) {
-            const int j = ks * OWN + o, c = c0 + j * 16 + q * 4;
-            const f32x4 v = total(j);
+        for (int o = 0; o < SHARE; ++o) {
+            const int u = o * KS + ks, j = u % SETS, i = u / SETS;
+            if (u >= SETS * MF) break;
+            const f32x4 v = total(j, i);
+            const int r = i * 16 + r16, c = c0 + j * 16 + q * 4;
+            if (r >= t.rows || c >= p.n) continue;  // n is a multiple of 8: all four or none
             uint2 pair;
             pair.x = pack_bf16(v[0], v[1]);
             pair.y = pack_bf16(v[2], v[3]);
-            if (inside && c < p.n) *reinterpret_cast<uint2 *>(out + c) = pair;  // n is a multiple of 8: all four or none
+            *reinterpret_cast<uint2 *>(out + (t.first + r) * p.n + c) = pair;
         }
     } else {
-        f32x4 a[OWN];
-        float top = 0.0f;
+        f32x4 a[SHARE];
 #pragma unroll
-        for (int o = 0; o < OWN; ++o) {
-            const f32x4 g = total(ks * OWN + o), u = total(2 + ks * OWN + o);
+        for (int o = 0; o < SHARE; ++o) {
+            const int u = o * KS + ks, j = u % SETS, i = u / SETS;
+            if (u >= SETS * MF) break;
+            const f32x4 g = total(j, i), v = total(2 + j, i);
+            float top = 0.0f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
-                a[o][k] = g[k] / (1.0f + expf(-g[k])) * u[k];
+                a[o][k] = g[k] / (1.0f + expf(-g[k])) * v[k];
                 top = fmaxf(top, fabsf(a[o][k]));
             }
+            top = fmaxf(top, __shfl_xor(top, 16));
+            top = fmaxf(top, __shfl_xor(top, 32));
+            if (q == 0) s_top[group][j][i * 16 + r16] = top;
         }
-        top = fmaxf(top, __shfl_xor(top, 16));
-        top = fmaxf(top, __shfl_xor(top, 32));
-        if (q == 0) s_top[wave][r16] = top;
         __syncthreads();
-        float m = kE4m3AmaxFloor;
+        uint8_t *out = static_cast<uint8_t *>(p.out);
 #pragma unroll
-        for (int j = 0; j < NG * KS; ++j) m = fmaxf(m, s_top[j][r16]);
-        const float inv = kE4m3Max / m;
-        if (!inside) return;
-        if (wave == 0 && q == 0) p.out_scales[(t.first + r16) * (p.n / kScaleBlock) + col_tile] = m / kE4m3Max;
-        uint8_t *out = static_cast<uint8_t *>(p.out) + (t.first + r16) * p.n + c0 + ks * OWN * 16 + q * 4;
+        for (int o = 0; o < SHARE; ++o) {
+            const int u = o * KS + ks, j = u % SETS, i = u / SETS;
+            if (u >= SETS * MF) break;
+            const int r = i * 16 + r16;
+            if (r >= t.rows) continue;
+            float m = kE4m3AmaxFloor;
 #pragma unroll
-        for (int o = 0; o < OWN; ++o)
-            *reinterpret_cast<uint32_t *>(out + o * 16) =
+            for (int n = 0; n < NG * SETS; ++n) m = fmaxf(m, s_top[n / SETS][n % SETS][r]);
+            const float inv = kE4m3Max / m;
+            if (group == 0 && j == 0 && q == 0)
+                p.out_scales[(t.first + r) * (p.n / kScaleBlock) + col_tile] = m / kE4m3Max;
+            *reinterpret_cast<uint32_t *>(out + (t.first + r) * p.n + c0 + j * 16 + q * 4) =
                 e4m3_pack4(a[o][0] * inv, a[o][1] * inv, a[o][2] * inv, a[o][3] * inv);
+        }
     }
 }
 
@@ -580,24 +620,46 @@ struct Plan {
     int threads, rows, cols;
 };
 
-// By the mean rows of an expert (all that the host knows of the sizes).  Measured over 32 experts, SwiGLU
-// of 7168 channels to 2048 and product of 2048 to 7168:
+template <bool SWIGLU, int MF, int NG, int KS, int WAVES>
+Plan narrow() {
+    return {expert_gemm_narrow_kernel<SWIGLU, MF, NG, KS, WAVES>, NG * KS * kWave, 16 * MF, SWIGLU ? 128 : 64 * NG};
+}
+
+// The choice rests on the mean rows of an expert, all that the host knows of the sizes.  Measured
+// over 32 experts, SwiGLU of 7168 channels to 2048 and product of 2048 to 7168, us:
 //   mean rows            4    8   12   16   32   64   96  128  192  256  512
-//   SwiGLU   narrow    177  179  239  236  360                              us
-//            wide 128  186  187  189  190  194  216  251  408  503  607 1092
-//   product  narrow     85   90  100  114  176                              us
-//            wide 128  103  104  106  105  109  115  119  156  187  233  396
+//   SwiGLU   narrow    177  179  239  236  360
+//            wide 128       187  170  170  172  219  263  405  484  600 1060
+//   product  narrow     85   90  100  114  176
+//            wide 128       104  103  103  105  106  113  146  178  219  387
 //            wide 256                           122  125  137  155  195  335
-// Up to 8 rows the narrow kernel leads; 128 rows a block serve until experts fill more than one.
+// Where there are fewer blocks than compute units a block's own time counts.  One expert, product of
+// 7168 channels to 2048 and of 2048 to 7168, us:
+//   rows                 1   16   64  128  256  512 1024 2048 4096 |   1   64  256 1024 2048 4096
+//   split (32 rows)     19   23   27   27   27   52  101  198  393 |   8   10   36  118  230  460
+//   wide 128                 36   39   59   59   59   59   63   84 |       15   21   23   44   94
+//   wide 256                            96   96   96   96   96  101 |            31   32   38   77
+// and SwiGLU of 7168 to 2048 takes 80 narrow, 57 wide up to 64 rows.
+constexpr int kComputeUnits = 256;
 Plan plan(const GemmArgs &a) {
-    const int mean = a.num_rows / a.num_experts;
+    const int64_t mean = a.num_rows / a.num_experts;
     if (a.swiglu) {
-        if (mean <= 8) return {expert_gemm_narrow_kernel<true, 4, 1>, 4 * kWave, 16, 128};
+        // a block for every compute unit, or the wide kernel's coalesced loads are faster
+        if (mean <= 8 && row_tiles(a, 16) * (a.n / 128) >= kComputeUnits) return narrow<true, 1, 4, 1, 3>();
         return {expert_gemm_wide_kernel<true, 2>, kBlockThreads, 128, 128};
     }
-    if (mean <= 8) return {expert_gemm_narrow_kernel<false, 2, 2>, 4 * kWave, 16, 128};
-    if (mean <= 112) return {expert_gemm_wide_kernel<false, 2>, kBlockThreads, 128, kBN};
-    return {expert_gemm_wide_kernel<false, 4>, kBlockThreads, 256, kBN};
+    if (row_tiles(a, 32) * ((a.n + 63) / 64) <= 2 * kComputeUnits) return narrow<false, 2, 1, 8, 2>();
+    if (mean <= 8) return narrow<false, 1, 2, 2, 3>();
+    // rounds of blocks over the compute units, a round of 256 rows 1.5 times one of 128; a segment's
+    // last tile is half full on average
+    auto rounds = [&](int rows) {
+        const int64_t cols = (a.n + kBN - 1) / kBN;
+        const int64_t halves = a.num_experts == 1 ? 2 * (((int64_t)a.num_rows + rows - 1) / rows)
+                                                  : a.num_experts + 2 * (int64_t)a.num_rows / rows;
+        return (halves * cols + 2 * kComputeUnits - 1) / (2 * kComputeUnits);
+    };
+    if (3 * rounds(256) <= 2 * rounds(128)) return {expert_gemm_wide_kernel<false, 4>, kBlockThreads, 256, kBN};
+    return {expert_gemm_wide_kernel<false, 2>, kBlockThreads, 128, kBN};
 }
 
 int64_t grid_blocks(const GemmArgs &a, const Plan &pl) {

@@ -102,21 +102,37 @@ def test_product_many_experts(rows, E):
     assert status == 0
 
 
-@pytest.mark.parametrize("mean", [1, 8, 9, 64, 112, 113, 300])
+# (experts, rows, n, k): every kernel of the product (split channels, few rows of many experts, 128 and 256 rows a
+# block) and of the SwiGLU form (few rows of many experts, 128 rows a block)
+KERNELS = [(1, 3, 256, 640), (3, 90, 256, 640), (40, 130, 1024, 384), (70, 100, 2048, 128), (6, 700, 2048, 256),
+           (3, 900, 1024, 128), (2, 1300, 8192, 128), (1, 4400, 2048, 128)]
+
+
+@pytest.mark.parametrize("case", KERNELS, ids=str)
 @pytest.mark.parametrize("exact", [True, False])
-def test_rows_an_expert_on_both_sides_of_each_choice_of_kernel(mean, exact):
-    """Both outputs at mean segment sizes around those where another kernel takes over, uneven around the mean."""
-    rng = np.random.default_rng(mean)
-    E, n, k = 3, 256, 640
-    rows = mean * E + 2
-    sizes = [rows - 2 * (mean // 2), mean // 2, mean // 2]
-    x, xs, w, ws = _inputs(rng, E, 2 * n, k, rows, exact)
-    got, _ = _product(E, 2 * n, k, x, xs, w, ws, sizes, rows)
+def test_each_kernel(case, exact):
+    """Both outputs, segments uneven around their mean, some empty."""
+    E, rows, n, k = case
+    rng = np.random.default_rng(rows)
+    print(f"[product] kernels {case} exact={exact}", flush=True)
+    share = rng.random(E) * (rng.random(E) < 0.8) + 1e-9
+    sizes = rng.multinomial(rows, share / share.sum())
+    x, xs, w, ws = _inputs(rng, E, n, k, rows, exact)
+    got, status = _product(E, n, k, x, xs, w, ws, sizes, rows)
     want, mag = oracle64.product(x, xs, w, ws, sizes, rows)
-    _check_product(got, want, mag, k, exact, None if exact else oracle64.product_cut(x, xs, w, ws, sizes, rows))
     if exact:
-        xs = xs / 64
-        want = want / 64
+        _check_product(got, want, mag, k, True)
+    else:  # the cut is measured for the first rows and the last alone: it is k / 8 products of the whole
+        at = np.r_[0:min(rows, 20), max(rows - 20, 0):rows]
+        ends = np.cumsum(sizes)
+        owner = np.searchsorted(ends, at, side="right")
+        cut = np.stack([oracle64.product_cut(x[r:r + 1], xs[r:r + 1], w[e:e + 1], ws[e:e + 1], [1], 1)[0]
+                        for r, e in zip(at, owner)])
+        _check_product(got[torch.from_numpy(at).cuda()], want[at], mag[at], k, False, cut)
+    assert status == 0
+    if exact:
+        xs, want = xs / 64, want / 64
+    n //= 2
     codes, scales, _ = _product(E, n, k, x, xs, w, ws, sizes, rows, swiglu=True)
     slack = np.zeros_like(want) if exact else (2 * (k + k // 128) + 2) * U * mag
     _check_swiglu(codes, scales, want, slack, np.ones(rows, bool))

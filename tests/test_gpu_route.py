@@ -59,6 +59,56 @@ def test_choice_and_weights(E, kind, dtype, renorm):
         assert status == 0
 
 
+# 2048 tokens and more go 16 lanes to a token, where they hold its experts (256), slots (16) and groups (16)
+MANY = [(16, 2, 1, 1), (60, 6, 1, 1), (64, 6, 8, 3), (65, 4, 5, 2), (128, 8, 16, 5), (160, 8, 8, 3), (192, 3, 6, 2),
+        (256, 8, 8, 4), (256, 16, 16, 16), (256, 17, 4, 2), (256, 8, 32, 9), (257, 8, 1, 1), (12, 16, 3, 2)]
+
+
+@pytest.mark.parametrize("E,k,groups,kept", MANY)
+@pytest.mark.parametrize("kind,dtype,with_bias", [("sigmoid", torch.float32, True), ("softmax", torch.bfloat16, False),
+                                                  ("softmax", torch.float32, True), ("sigmoid", torch.bfloat16, True)])
+def test_many_tokens(E, k, groups, kept, kind, dtype, with_bias):
+    rng = np.random.default_rng(E + k)
+    T = 2049
+    print(f"[route] many tokens E={E} k={k} G={groups} {kind} {dtype} bias={with_bias}", flush=True)
+    values, logits = _logits(rng, T, E, dtype)
+    bias = (rng.standard_normal(E) * 0.1).astype(np.float32) if with_bias else None
+    mask = (rng.random(T) < 0.9).astype(np.uint8)
+    best = 2 if groups > 1 else 1
+    got_i, got_w, status = _route(logits, None if bias is None else torch.from_numpy(bias).cuda(), kind, k, groups,
+                                  kept, best, kind == "sigmoid", 1.5, torch.from_numpy(mask).cuda())
+    # the first tokens, the last ones and some between
+    at = np.unique(np.concatenate([np.arange(40), rng.integers(0, T, 60), np.arange(T - 20, T)]))
+    want_i, want_w = oracle64.route(values[at], bias, kind, k, groups, kept, best, kind == "sigmoid", 1.5, mask[at])
+    assert np.array_equal(got_i[at], want_i) and status == 0
+    _weights_near(got_w[at], want_w, kind, kind == "sigmoid")
+    gw = rng.standard_normal((T, k)).astype(np.float32)
+    out = torch.full((T, E), float("nan"), dtype=dtype, device="cuda")
+    experts.ep_route_backward(ep.make_shape(T, 8, k, E, 1, 1), experts.make_router(KINDS[kind], 1, 1, 1, kind == "sigmoid", 1.5),
+                              logits, torch.from_numpy(got_i).cuda(), torch.from_numpy(gw).cuda(), out)
+    assert bool(out.isfinite().all())
+    _check_gradient(out[torch.from_numpy(at).cuda()], values[at], got_i[at], gw[at], kind, kind == "sigmoid", 1.5)
+
+
+@pytest.mark.parametrize("T", [70, 2100])
+@pytest.mark.parametrize("kind", sorted(KINDS))
+def test_near_ties_among_many_and_few_tokens(T, kind):
+    """Biases that undo the scores' differences to a few steps of f32: every token's order is a near tie."""
+    rng = np.random.default_rng(T)
+    E, k = 64, 6
+    base = rng.standard_normal(E).astype(np.float32)
+    values = np.repeat(base[None], T, 0)
+    values += (rng.integers(-3, 4, size=(T, E)) * 2.0 ** -22).astype(np.float32)
+    p = oracle64.scores(base[None], kind)[0]
+    bias = (0.7 - p).astype(np.float32)
+    for groups, kept, best in ((1, 1, 1), (8, 3, 2), (8, 3, 1)):
+        got_i, got_w, _ = _route(torch.from_numpy(values).cuda(), torch.from_numpy(bias).cuda(), kind, k, groups, kept, best)
+        at = np.unique(np.concatenate([np.arange(40), rng.integers(0, T, 40)]))
+        want_i, want_w = oracle64.route(values[at], bias, kind, k, groups, kept, best, True, 1.0)
+        assert np.array_equal(got_i[at], want_i)
+        _weights_near(got_w[at], want_w, kind, True)
+
+
 @pytest.mark.parametrize("E,groups,kept", [(256, 8, 4), (64, 64, 9), (160, 8, 3), (12, 4, 4), (96, 2, 1), (1024, 16, 1)])
 @pytest.mark.parametrize("best", [1, 2])
 @pytest.mark.parametrize("kind", sorted(KINDS))
