@@ -23,7 +23,8 @@ ep_status_t router_checked(const ep_shape_t *s, const ep_router_t *r, int32_t lo
         r->groups_kept > r->num_groups || (r->group_best != 1 && r->group_best != 2) || !isfinite(r->weight_scale))
         return EP_ERR_INVALID_ARG;
     if (stride < s->num_experts) return EP_ERR_INVALID_ARG;
-    if (s->num_experts > kMaxRouteExperts || r->num_groups > kMaxRouteGroups) return EP_ERR_UNSUPPORTED;
+    if (s->num_experts > kMaxRouteExperts || r->num_groups > kMaxRouteGroups || s->num_tokens > kMaxRouteTokens)
+        return EP_ERR_UNSUPPORTED;
     return EP_OK;
 }
 

@@ -9,6 +9,7 @@ namespace ep {
 
 constexpr int kMaxRouteExperts = 2048;
 constexpr int kMaxRouteGroups = 64;  // one group per lane of a wave
+constexpr int kMaxRouteTokens = 1 << 25;  // a wave each stays within a grid of 2^32 threads
 constexpr int kMaxGemmExperts = 16384;
 constexpr int kMaxGemmK = 1 << 20;  // a tile's rows are within reach of a 32-bit offset
 constexpr int kScaleBlock = 128;  // channels (and weight rows) per scale

@@ -567,6 +567,17 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_backward_kernel(Rout
     const int64_t t = (int64_t)blockIdx.x * kRouteWaves * kTokens + threadIdx.x / LPT;
     const bool here = t < p.T;
     const int64_t row = t * p.a.stride;
+    // lane j: slot j's expert (num_topk <= LPT, which the launcher sees to)
+    int id = -1;
+    bool bad_id = false;
+    if (here && at < p.K) {
+        const int64_t e = p.a.topk_idx[t * p.K + at];
+        bad_id = e < -1 || e >= p.E;
+        if (e >= 0 && e < p.E) id = (int)e;
+    }
+    if (ballot64(bad_id) != 0ull && lane == 0) flag(p.a.dev_status, EP_DEV_BAD_TOPK_IDX);
+    // a token without slots has a gradient of zeros, whatever its logits: they are not read
+    const bool on = token_bits<LPT>(ballot64(id >= 0), lane) != 0ull;
     float logit[VPL];
     bool bad = false;
     auto load = [&](int from) {  // -inf where there is no usable logit
@@ -574,11 +585,11 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_backward_kernel(Rout
         for (int i = 0; i < VPL; ++i) logit[i] = -INFINITY;
         const int e = from + at * VPL;
         if (p.vector) {  // a lane's logits are whole aligned words, and all of them in or out
-            if (here && e < p.E) load_logits<VPL, BF16>(p.a.logits, row + e, logit);
+            if (on && e < p.E) load_logits<VPL, BF16>(p.a.logits, row + e, logit);
         } else {
 #pragma unroll
             for (int i = 0; i < VPL; ++i)
-                if (here && e + i < p.E) logit[i] = load_logit<BF16>(p.a.logits, row + e + i);
+                if (on && e + i < p.E) logit[i] = load_logit<BF16>(p.a.logits, row + e + i);
         }
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
@@ -612,23 +623,14 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_backward_kernel(Rout
         sum = token_sum<LPT>(sum);
     }
 
-    // lane j: slot j's expert, its score and the gradient of that score, in 64 bits: the sums over
-    // the slots cancel (num_topk <= LPT, which the launcher sees to)
-    int id = -1;
+    // lane j: the score of slot j's expert and its gradient, in 64 bits: the sums over the slots cancel
     double s = 0.0, g = 0.0;
-    bool bad_id = false;
-    if (here && at < p.K) {
-        const int64_t e = p.a.topk_idx[t * p.K + at];
-        bad_id = e < -1 || e >= p.E;
-        if (e >= 0 && e < p.E) {
-            id = (int)e;
-            const float l = load_logit<BF16>(p.a.logits, row + id);
-            if (l > -INFINITY && !unusable(l))
-                s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)top) / (double)sum;
-            g = p.a.grad_w[t * p.K + at];
-        }
+    if (id >= 0) {
+        const float l = load_logit<BF16>(p.a.logits, row + id);
+        if (l > -INFINITY && !unusable(l))
+            s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)top) / (double)sum;
+        g = p.a.grad_w[t * p.K + at];
     }
-    if (ballot64(bad_id) != 0ull && lane == 0) flag(p.a.dev_status, EP_DEV_BAD_TOPK_IDX);
     double ds = g * (double)p.scale;
     if (p.renorm) {
         const double all = token_sum<LPT>(s), gs = token_sum<LPT>(g * s);

@@ -71,8 +71,8 @@ typedef struct {
  *      (logits_stride >= E); bias [E] f32 (nullable); token_mask [t] uint8 (nullable; 0 = the
  *      token is not routed and its logits are not read).
  * Out: topk_idx [t][k] int64, topk_weights [t][k] f32.
- * Limits: num_experts <= 2048 (EP_ERR_UNSUPPORTED).  Logits, bias and topk_weights 4-byte
- * aligned (bf16 logits 2-byte), topk_idx 8-byte aligned.  One launch.
+ * Limits: num_experts <= 2048, num_tokens <= 2^25 (EP_ERR_UNSUPPORTED).  Logits, bias and
+ * topk_weights 4-byte aligned (bf16 logits 2-byte), topk_idx 8-byte aligned.  One launch.
  * dev_status (nullable): EP_DEV_BAD_LOGIT.
  */
 ep_status_t ep_route(const ep_shape_t *s, const ep_router_t *r, const void *logits, int32_t logits_type,
@@ -86,8 +86,8 @@ ep_status_t ep_route(const ep_shape_t *s, const ep_router_t *r, const void *logi
  *   ds_j = weight_scale * g_j                                 otherwise
  *   grad_logits[t][e] = s_e (1 - s_e) * (sum of ds_j over the slots naming e)          sigmoid
  *   grad_logits[t][e] = s_e * (sum of ds_j over the slots naming e - sum_j ds_j s_{e_j})  softmax
- * Slots of -1 have no part (a token whose slots are all -1 gets a row of zeros); an expert named
- * by several slots gets the sum.  A logit that is not finite gets 0.
+ * Slots of -1 have no part (a token whose slots are all -1 gets a row of zeros, and its logits are
+ * not read); an expert named by several slots gets the sum.  A logit that is not finite gets 0.
  * In:  logits as ep_route took them; topk_idx [t][k] as it wrote them; grad_weights [t][k] f32.
  * Out: grad_logits, rows of E values of logits_type at a stride of grad_stride elements, written
  *      whole (elements between rows are not touched).  May not overlap logits.

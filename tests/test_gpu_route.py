@@ -319,6 +319,27 @@ def test_gradient_of_masked_and_bad_logits():
         _check_gradient(out, bad, idx, gw, kind, renorm, 1.0)
 
 
+@pytest.mark.parametrize("T", [40, 2100])
+def test_gradient_of_tokens_without_slots_reads_no_logits(T):
+    """A padded batch: NaN logits where the mask left no slot are neither flagged nor passed on."""
+    rng = np.random.default_rng(6)
+    E, k = 60, 4
+    values, logits = _logits(rng, T, E, torch.float32)
+    mask = (rng.random(T) < 0.5).astype(np.uint8)
+    logits[torch.from_numpy(mask == 0).cuda()] = float("nan")
+    for kind, renorm in itertools.product(sorted(KINDS), (False, True)):
+        idx, _, status = _route(logits, None, kind, k, renorm=renorm, mask=torch.from_numpy(mask).cuda())
+        assert status == 0 and np.all(idx[mask == 0] == -1)
+        gw = rng.standard_normal((T, k)).astype(np.float32)
+        out = torch.full((T, E), float("nan"), device="cuda")
+        word = torch.zeros(1, dtype=torch.int32, device="cuda")
+        experts.ep_route_backward(ep.make_shape(T, 8, k, E, 1, 1), experts.make_router(KINDS[kind], 1, 1, 1, renorm), logits,
+                                  torch.from_numpy(idx).cuda(), torch.from_numpy(gw).cuda(), out, word)
+        assert int(word.item()) == 0 and not out[torch.from_numpy(mask == 0).cuda()].any()
+        at = np.flatnonzero(mask)[:30]
+        _check_gradient(out[torch.from_numpy(at).cuda()], values[at], idx[at], gw[at], kind, renorm, 1.0)
+
+
 def test_no_tokens_and_many_slots():
     empty = torch.empty(0, 16, device="cuda")
     idx, w, status = _route(empty, None, "sigmoid", 4)
