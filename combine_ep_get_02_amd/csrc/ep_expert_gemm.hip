@@ -174,15 +174,16 @@ __global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(Gemm
     constexpr int kStep = kBlockThreads / kUnits;
     const int r0 = threadIdx.x / kUnits, c0 = rotate(r0, threadIdx.x & (kUnits - 1)) * 16;
     static_assert(kStep % 32 == 0, "a step keeps a row's rotation");
-    const int x_first = r0 * p.k + c0;
-    int w_first;
+    const uint32_t k = p.k;  // unsigned: a row past the end may lie past 2^31, and must not come out below 0
+    const uint32_t x_first = r0 * k + c0;
+    uint32_t w_first;
     if constexpr (SWIGLU) {
         // half of a wave's weight rows are gate rows, half the up rows of the same outputs
         static_assert(kStep % (2 * HALF) == 0, "a step keeps a row's place in its half");
         const int c = col_tile * 128 + r0 / (2 * HALF) * HALF + r0 % HALF;
-        w_first = ((r0 & HALF) ? p.n + c : c) * p.k + c0;
+        w_first = (uint32_t)((r0 & HALF) ? p.n + c : c) * k + c0;
     } else {
-        w_first = (col_tile * kBN + r0) * p.k + c0;
+        w_first = (uint32_t)(col_tile * kBN + r0) * k + c0;
     }
     int scale_row0, scale_row1;  // of the first and the second 128 weight rows; gate and up
     if constexpr (SWIGLU) {
@@ -195,7 +196,7 @@ __global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(Gemm
     const __amdgpu_buffer_rsrc_t sbuf =
         wave * kWave < BM ? descriptor(p.x_scales + t.first * blocks, (uint32_t)t.rows * blocks * 4)
                           : descriptor(p.w_scales + (int64_t)t.expert * scale_rows * blocks, (uint32_t)scale_rows * blocks * 4);
-    const int sat = (wave * kWave < BM ? (int)threadIdx.x : (lane & 1) ? scale_row1 : scale_row0) * blocks * 4;
+    const uint32_t sat = (wave * kWave < BM ? (int)threadIdx.x : (lane & 1) ? scale_row1 : scale_row0) * blocks * 4;
 
     f32x16 acc[MI][2];
 #pragma unroll
@@ -210,17 +211,18 @@ __global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(Gemm
     // Past the last block the loads go on, from behind the descriptors' ends (they fetch nothing):
     // that every step issues the same number is what lets the waits count.
     auto load = [&](u32x4 *to, int b) {
-        const int past = b < blocks ? 0 : INT_MIN, from = b < blocks ? b : 0;
-        int xat = x_first, wat = w_first;
+        const uint32_t past = b < blocks ? 0u : 0x80000000u;
+        const int from = b < blocks ? b : 0;
+        uint32_t xat = x_first, wat = w_first;
         asm volatile("" : "+v"(xat), "+v"(wat));  // addresses are cheaper formed anew than kept in registers
 #pragma unroll
         for (int i = 0; i < XL; ++i)
-            load_to_lds(xbuf, to + kX + i * kBlockThreads + wave * kWave, xat + (i * kStep * p.k + past), from * kScaleBlock);
+            load_to_lds(xbuf, to + kX + i * kBlockThreads + wave * kWave, (int)(xat + (i * kStep * k + past)), from * kScaleBlock);
 #pragma unroll
         for (int i = 0; i < WL; ++i)
             load_to_lds(wbuf, to + kW + i * kBlockThreads + wave * kWave,
-                        wat + (i * (SWIGLU ? kStep / 2 : kStep) * p.k + past), from * kScaleBlock);
-        load_to_lds(sbuf, reinterpret_cast<float *>(to + kS) + wave * kWave, sat + past, from * 4);
+                        (int)(wat + (i * (SWIGLU ? kStep / 2 : kStep) * k + past)), from * kScaleBlock);
+        load_to_lds(sbuf, reinterpret_cast<float *>(to + kS) + wave * kWave, (int)(sat + past), from * 4);
     };
     // the lane's units of any row it reads: 2 u + half, where the rotation has put them
     const int unit0 = rotate(r32, half);
@@ -469,7 +471,7 @@ __global__ __launch_bounds__(NG *KS *kWave, WAVES) void expert_gemm_narrow_kerne
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
         const int row = SWIGLU ? (j < 2 ? c0 + j * 16 : p.n + c0 + (j - 2) * 16) : c0 + j * 16;
-        wat[j] = (row + r16) * p.k + q * 16;
+        wat[j] = (int)((uint32_t)(row + r16) * p.k + q * 16);  // unsigned: past the end, not below 0
     }
     const float *sw0 = p.w_scales + (int64_t)t.expert * scale_rows * blocks;
     const float *sw1;
