@@ -71,6 +71,8 @@ def _raw_stream(stream, device) -> int | None:
     # the handle alone: building torch's stream object costs as much as the rest of a small call
     if stream is None and device >= 0:
         return torch._C._cuda_getCurrentRawStream(device)
+    if isinstance(stream, torch.cuda.Stream) and stream.device_index != device:
+        raise ValueError(f"stream: on GPU {stream.device_index}, not on the current one")
     return _stream(stream)
 
 
@@ -94,6 +96,8 @@ def _refuse(name, t, wanted) -> None:
 
 def _logit_rows(name, t, tokens, experts, device, dtype=None) -> int:
     """The stride between rows of a [tokens][experts] tensor whose rows may lie apart."""
+    if t is None:
+        _refuse(name, t, f"[{tokens}][{experts}] of {dtype or 'float32 or bfloat16'}")
     rows, columns = t.shape if t.dim() == 2 else (-1, -1)
     apart, along = t.stride() if t.dim() == 2 else (0, 0)
     if t.get_device() != device or t.dtype not in _LOGITS or (dtype is not None and t.dtype != dtype) or \

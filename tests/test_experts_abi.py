@@ -115,6 +115,8 @@ def test_bad_route_arguments_refused(ep, lib):
     assert _route_bwd(lib, many, r, stride=2056, out_stride=2056) == ep.EP_ERR_UNSUPPORTED
     groups = _shape(ep, num_experts=128 * 8)
     assert _route(lib, groups, experts.make_router(1, num_groups=128), stride=1024) == ep.EP_ERR_UNSUPPORTED
+    many = _shape(ep, num_tokens=(1 << 25) + 1, num_ranks=1)
+    assert _route(lib, many, r) == ep.EP_ERR_UNSUPPORTED and _route_bwd(lib, many, r) == ep.EP_ERR_UNSUPPORTED
     none = _shape(ep, num_tokens=0)
     assert _route(lib, none, r, logits=None, idx=None, w=None, bias=None, mask=None) == ep.EP_OK
     assert _route_bwd(lib, none, r, logits=None, idx=None, g=None, out=None) == ep.EP_OK
@@ -136,7 +138,8 @@ def test_bad_product_arguments_refused(ep, lib, swiglu):
     if swiglu:
         for kw in (dict(n=192), dict(outs=None), dict(outs=ODD2)):
             assert _gemm(lib, swiglu, **kw) == bad, kw
-    for kw in (dict(experts=16385), dict(n=1 << 16, k=1 << 15), dict(n=1 << 14, num_rows=2147483647)):
+    for kw in (dict(experts=16385), dict(n=1 << 16, k=1 << 15), dict(k=(1 << 20) + 128),
+               dict(n=1 << 14, num_rows=2147483647)):
         assert _gemm(lib, swiglu, **kw) == ep.EP_ERR_UNSUPPORTED, kw
     empty = dict(x=None, xs=None, w=None, ws=None, out=None, outs=None, num_rows=0)
     assert _gemm(lib, swiglu, **empty) == ep.EP_OK
@@ -177,7 +180,7 @@ def test_binding_refuses_tensors_the_library_cannot_check(ep):
     r = experts.make_router(experts.EP_SCORE_SIGMOID)
     cpu = torch.zeros(64, 64)
     idx, w = torch.zeros(64, 4, dtype=torch.int64), torch.zeros(64, 4)
-    for logits in (cpu, cpu.double(), cpu[:32], cpu[:, :32], cpu.view(-1)):
+    for logits in (None, cpu, cpu.double(), cpu[:32], cpu[:, :32], cpu.view(-1)):
         with pytest.raises(ValueError):
             experts.ep_route(s, r, logits, None, None, idx, w)
     with pytest.raises(ValueError):

@@ -211,3 +211,44 @@ def test_rows_of_random_bits_through_the_layer():
     layer.run()
     layer.outputs()
     assert bool(layer.b.combined_x.isfinite().all())
+
+
+def test_a_layer_without_tokens():
+    layer = Layer(T=0, H=256, I=128, E=8, R=2, K=2, seed=11)
+    layer.run()
+    torch.cuda.synchronize()
+    assert int(layer.b.dev_status.item()) == 0
+
+
+def test_a_layer_whose_buffers_are_larger_than_its_rows():
+    """Receive and grouped capacity far above what the routing fills: the same outputs."""
+    layer = Layer(T=50, H=256, I=128, E=16, R=4, K=3, align=2, seed=12)
+    layer.draw(2)
+    layer.run()
+    want = layer.outputs()
+    layer.b = ep.allocate(layer.shape, 50 * 4 + 300)
+    layer.e = experts.allocate_experts(layer.b, 128, 5000)
+    layer.e.y.fill_(float("nan"))
+    layer.run()
+    for got, ref in zip(layer.outputs(), want):
+        assert torch.equal(got, ref)
+
+
+def test_few_received_rows_are_dropped_and_flagged():
+    """A receive capacity below the routing: the tokens that fit come out, nothing reads past the buffers."""
+    layer = Layer(T=50, H=256, I=128, E=16, R=4, K=3, seed=13)
+    layer.draw(2)
+    layer.run()
+    whole = layer.outputs()[0]
+    n = int(layer.b.num_recv.item())
+    layer.b = ep.allocate(layer.shape, n - 20)
+    layer.e = experts.allocate_experts(layer.b, 128, 150)
+    layer.run()
+    torch.cuda.synchronize()
+    assert int(layer.b.dev_status.item()) == ep.EP_DEV_RECV_OVERFLOW
+    kept = (layer.b.send_slot >= 0).cpu().numpy()
+    idx = layer.e.topk_idx.cpu().numpy()
+    fits = np.array([all(kept[t, e // 4] for e in idx[t]) for t in range(50)])
+    assert fits.any() and not fits.all()
+    got = layer.b.combined_x.view(torch.int16).cpu()
+    assert torch.equal(got[torch.from_numpy(fits)], whole[torch.from_numpy(fits)])
