@@ -160,7 +160,8 @@ ep_status_t ep_expert_gemm_swiglu_fp8(int32_t num_experts, int32_t n, int32_t k,
  *      send_slot [t][R] and slot_pos [num_recv_rows][k] as ep_dispatch_grouped (or ep_dispatch and
  *      ep_group_by_expert) wrote them.  num_recv_rows and num_grouped_rows are the rows allocated.
  * Out: combined_x [t][h] bf16 (a token without rows gets zeros).
- * y and combined_x 16-byte, topk_idx 8-byte, the others 4-byte aligned.  One launch.
+ * y and combined_x 16-byte, topk_idx 8-byte, the others 4-byte aligned.  One launch.  Limit: fewer
+ * than 2^23 KiB pieces in the tokens' rows, each row rounded up (EP_ERR_UNSUPPORTED).
  * dev_status (nullable): EP_DEV_BAD_TOPK_IDX (an id outside [-1, E)), EP_DEV_BAD_SEND_SLOT (a
  * send_slot outside [-1, num_recv_rows) or a slot_pos outside [-1, num_grouped_rows)); such slots
  * are skipped.
@@ -180,7 +181,7 @@ ep_status_t ep_combine_grouped(const ep_shape_t *s, const void *y, const int64_t
  *      the grouping wrote them; the rest as for ep_combine_grouped.
  * Out: grad_y [num_grouped_rows][h] bf16; grad_topk_weights [t][k] f32, which ep_route_backward
  *      takes as grad_weights.  grad_y may not overlap y.
- * Alignment and dev_status as for ep_combine_grouped.  One launch.
+ * Alignment, limit and dev_status as for ep_combine_grouped.  One launch.
  */
 ep_status_t ep_combine_grouped_backward(const ep_shape_t *s, const void *grad_combined, const void *y,
                                         const int64_t *topk_idx, const float *topk_weights, const int32_t *send_slot,
