@@ -430,23 +430,27 @@ __global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(Gemm
     }
 }
 
-// Few rows: 16 MF rows x 64 NG weight rows a block of NG x KS waves, WAVES of them a SIMD.  Each wave
-// reads weights of its own, once, so they go straight to registers: no LDS, no barrier, and every
-// wave has the next block of channels on its way while it multiplies one.  The KS waves of a group
-// take every KS-th block of channels and add up through LDS at the end.
+// Few rows: 16 MF rows x 16 WF NG weight rows a block of NG x KS waves, WAVES of them a SIMD.  Each wave
+// reads weights of its own, once, into registers, DEEP blocks of channels at a time, and there are no
+// barriers: a wave has loads under way while it multiplies.  The KS waves of a group take every KS-th
+// block of channels and add up through LDS at the end.
 //
-// With rows for many experts this is bound by the weights' bytes: 128 rows of 32 experts take 175 us
-// for 0.94 GB (SwiGLU) and 82-85 us for 0.47 GB, 5.4 to 5.7 TB/s.  (Three waves a SIMD hold all they
-// keep in registers; four spill, and 8-wave blocks wait longer at their end: 97-100 us for the
-// second.)  Neighbouring lanes read different rows, 16 bytes each, which one compute unit takes at 16
-// bytes a clock -- enough for all of them together, little for a few blocks alone.  There the waves of
-// a block share the channels eight ways: 16 rows x 2048 of 7168 channels 44 -> 22 us.
-template <bool SWIGLU, int MF, int NG, int KS, int WAVES>
+// With rows for many experts this is bound by the weights' bytes: 128 rows of 32 experts take 168 us
+// for 0.94 GB (SwiGLU, 7168 channels to 2048) and 81 us for 0.47 GB (product, 2048 to 7168), 5.5 and
+// 5.8 TB/s.  A few blocks alone are bound by what one compute unit takes in: 16 bytes a clock where
+// neighbouring lanes read different rows, as the matrix instructions want them, and over 30 where eight
+// lanes read a row's 128 bytes.  So they do that, and the wave turns its tile round in LDS that no other
+// wave touches (16 rows of one expert, 2048 of 7168 channels: 23 -> 13 us; the SwiGLU above 180 -> 168).
+template <bool SWIGLU, int MF, int WF, int NG, int KS, int DEEP, int WAVES>
 __global__ __launch_bounds__(NG *KS *kWave, WAVES) void expert_gemm_narrow_kernel(GemmArgs p, int col_tiles) {
-    static_assert(!SWIGLU || NG == 4, "a block holds a scale's 128 outputs");
-    constexpr int BM = 16 * MF, BN = 64 * NG;
-    constexpr int SETS = SWIGLU ? 2 : 4;  // 16 columns of output each, of a group
-    __shared__ f32x4 s_sum[NG][KS][4][MF][kWave];
+    static_assert(!SWIGLU || 8 * WF * NG == 128, "a block holds a scale's 128 outputs");
+    constexpr int BM = 16 * MF, BN = 16 * WF * NG;
+    constexpr int SETS = SWIGLU ? WF / 2 : WF;  // 16 columns of output each, of a group
+    constexpr int XL = 2 * MF, WL = 2 * WF;     // loads of a block's rows and weight rows, 8 rows each
+    constexpr int kTile = (XL + WL) * kWave;
+    constexpr int kSums = WF * MF * kWave;
+    constexpr int kShare = kTile > kSums ? kTile : kSums;  // of a wave: its tile, then its sums
+    __shared__ u32x4 s_tile[NG * KS][kShare];
     __shared__ float s_top[NG][SETS][BM];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -464,15 +468,14 @@ __global__ __launch_bounds__(NG *KS *kWave, WAVES) void expert_gemm_narrow_kerne
     // rows past the segment and weight rows past the last are past the descriptors' ends: they read
     // as 0 and are not stored
     const int q = lane >> 4, r16 = lane & 15;
-    const int xat = r16 * p.k + q * 16, sat = r16 * blocks * 4;
-    // column (output) of the group's first weight row; SWIGLU: rows 0-31 are gate rows, 32-63 the up rows of the same
-    const int c0 = SWIGLU ? col_tile * 128 + group * 32 : col_tile * BN + group * 64;
-    int wat[4];
-#pragma unroll
-    for (int j = 0; j < 4; ++j) {
-        const int row = SWIGLU ? (j < 2 ? c0 + j * 16 : p.n + c0 + (j - 2) * 16) : c0 + j * 16;
-        wat[j] = (int)((uint32_t)(row + r16) * p.k + q * 16);  // unsigned: past the end, not below 0
-    }
+    const uint32_t k = p.k;  // unsigned: a row past the end may lie past 2^31, and must not come out below 0
+    const int sat = r16 * blocks * 4;
+    // column (output) of the group's first weight row; SWIGLU: half are gate rows, half the up rows of the same
+    const int c0 = SWIGLU ? col_tile * 128 + group * 8 * WF : col_tile * BN + group * 16 * WF;
+    // eight lanes load a row's 128 bytes, unit c of row r to place c ^ (r / 2) % 8 of its row in LDS
+    const int r8 = lane >> 3;
+    const uint32_t unit[2] = {(uint32_t)((lane & 7) ^ (r8 >> 1)) * 16, (uint32_t)((lane & 7) ^ (r8 >> 1) ^ 4) * 16};
+    const uint32_t xat = r8 * k, wat = (uint32_t)(c0 + r8) * k;
     const float *sw0 = p.w_scales + (int64_t)t.expert * scale_rows * blocks;
     const float *sw1;
     if constexpr (SWIGLU) {
@@ -484,38 +487,56 @@ __global__ __launch_bounds__(NG *KS *kWave, WAVES) void expert_gemm_narrow_kerne
     }
 
     struct Codes {
-        u32x4 w[4][2], x[MF][2];
+        u32x4 w[WL], x[XL];
         float sx[MF], sw[2];
     };
+    // Past the last block the loads go on, from behind the descriptors' ends (they fetch nothing):
+    // that every step issues the same number is what lets the waits count.
     auto load = [&](Codes &c, int b) {
+        const uint32_t past = b < blocks ? 0u : 0x80000000u;
+        const int from = b < blocks ? b : 0;
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            c.w[j][0] = __builtin_amdgcn_raw_buffer_load_b128(wbuf, wat[j], b * kScaleBlock, 0);
-            c.w[j][1] = __builtin_amdgcn_raw_buffer_load_b128(wbuf, wat[j] + 64, b * kScaleBlock, 0);
+        for (int i = 0; i < WL; ++i) {
+            const uint32_t row = SWIGLU && i >= WL / 2 ? p.n + (i - WL / 2) * 8 : i * 8;
+            c.w[i] = __builtin_amdgcn_raw_buffer_load_b128(wbuf, (int)(wat + row * k + unit[i & 1] + past), from * kScaleBlock, 0);
         }
 #pragma unroll
-        for (int i = 0; i < MF; ++i) {
-            c.x[i][0] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, xat + i * 16 * p.k, b * kScaleBlock, 0);
-            c.x[i][1] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, xat + i * 16 * p.k + 64, b * kScaleBlock, 0);
-            c.sx[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sbuf, sat + i * 16 * blocks * 4, b * 4, 0));
-        }
-        c.sw[0] = sw0[b];
-        c.sw[1] = SWIGLU ? sw1[b] : c.sw[0];
+        for (int i = 0; i < XL; ++i)
+            c.x[i] = __builtin_amdgcn_raw_buffer_load_b128(xbuf, (int)(xat + i * 8 * k + unit[i & 1] + past), from * kScaleBlock, 0);
+#pragma unroll
+        for (int i = 0; i < MF; ++i)
+            c.sx[i] = __uint_as_float(__builtin_amdgcn_raw_buffer_load_b32(sbuf, sat + i * 16 * blocks * 4, from * 4, 0));
+        c.sw[0] = sw0[from];
+        c.sw[1] = SWIGLU ? sw1[from] : c.sw[0];
     };
-    f32x4 acc[MF][4];
+    u32x4 *tile = s_tile[wave];
+    const int place = q ^ (r16 >> 1);
+    auto unit_of = [&](int row, int h) { return tile[(row + r16) * kUnits + (place ^ (4 * h))]; };
+    f32x4 acc[MF][WF];
 #pragma unroll
     for (int i = 0; i < MF; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
+        for (int j = 0; j < WF; ++j) acc[i][j] = f32x4{0.f, 0.f, 0.f, 0.f};
     auto multiply = [&](const Codes &c) {
 #pragma unroll
-        for (int j = 0; j < 4; ++j) {
+        for (int i = 0; i < WL; ++i) tile[i * kWave + lane] = c.w[i];
+#pragma unroll
+        for (int i = 0; i < XL; ++i) tile[(WL + i) * kWave + lane] = c.x[i];
+        u32x4 x[MF][2];
+#pragma unroll
+        for (int i = 0; i < MF; ++i) {
+            x[i][0] = unit_of(16 * (WF + i), 0);
+            x[i][1] = unit_of(16 * (WF + i), 1);
+        }
+#pragma unroll
+        for (int j = 0; j < WF; ++j) {
+            const u32x4 w[2] = {unit_of(j * 16, 0), unit_of(j * 16, 1)};
             f16x8 fw[4];
             if constexpr (SWIGLU) {
 #pragma unroll
                 for (int h = 0; h < 2; ++h) {
-                    fw[2 * h] = to_f16<0>(c.w[j][h]);
-                    fw[2 * h + 1] = to_f16<1>(c.w[j][h]);
+                    fw[2 * h] = to_f16<0>(w[h]);
+                    fw[2 * h + 1] = to_f16<1>(w[h]);
                 }
             }
 #pragma unroll
@@ -524,38 +545,43 @@ __global__ __launch_bounds__(NG *KS *kWave, WAVES) void expert_gemm_narrow_kerne
                 if constexpr (SWIGLU) {
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        part = __builtin_amdgcn_mfma_f32_16x16x32_f16(fw[2 * h], to_f16<0>(c.x[i][h]), part, 0, 0, 0);
-                        part = __builtin_amdgcn_mfma_f32_16x16x32_f16(fw[2 * h + 1], to_f16<1>(c.x[i][h]), part, 0, 0, 0);
+                        part = __builtin_amdgcn_mfma_f32_16x16x32_f16(fw[2 * h], to_f16<0>(x[i][h]), part, 0, 0, 0);
+                        part = __builtin_amdgcn_mfma_f32_16x16x32_f16(fw[2 * h + 1], to_f16<1>(x[i][h]), part, 0, 0, 0);
                     }
                 } else {
-                    part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(
-                        codes(c.w[j][0], c.w[j][1]), codes(c.x[i][0], c.x[i][1]), part, 0, 0, 0, 0, 0, 0);
+                    part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(codes(w[0], w[1]), codes(x[i][0], x[i][1]),
+                                                                            part, 0, 0, 0, 0, 0, 0);
                 }
-                const float s = c.sx[i] * c.sw[j >> 1];
+                const float s = c.sx[i] * c.sw[SWIGLU && j >= SETS];
 #pragma unroll
-                for (int k = 0; k < 4; ++k) acc[i][j][k] = __builtin_fmaf(part[k], s, acc[i][j][k]);
+                for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(part[e], s, acc[i][j][e]);
             }
         }
     };
-    Codes even, odd;
-    if (ks < blocks) load(even, ks);
-    for (int b = ks; b < blocks; b += 2 * KS) {
-        if (b + KS < blocks) load(odd, b + KS);
-        multiply(even);
-        if (b + 2 * KS < blocks) load(even, b + 2 * KS);
-        if (b + KS < blocks) multiply(odd);
+    Codes c[DEEP];
+#pragma unroll
+    for (int d = 0; d + 1 < DEEP; ++d) load(c[d], ks + d * KS);
+    for (int b = ks; b < blocks; b += DEEP * KS) {
+#pragma unroll
+        for (int d = 0; d < DEEP; ++d) {
+            load(c[(d + DEEP - 1) % DEEP], b + (d + DEEP - 1) * KS);
+            if (b + d * KS < blocks) multiply(c[d]);
+        }
     }
 
     // the KS sums of each 16 x 16 result, added in order; the waves of a group share its results out
 #pragma unroll
     for (int i = 0; i < MF; ++i)
 #pragma unroll
-        for (int j = 0; j < 4; ++j) s_sum[group][ks][j][i][lane] = acc[i][j];
+        for (int j = 0; j < WF; ++j) reinterpret_cast<f32x4 *>(tile)[(j * MF + i) * kWave + lane] = acc[i][j];
     __syncthreads();
     auto total = [&](int j, int i) {
-        f32x4 v = s_sum[group][0][j][i][lane];
+        auto part = [&](int k) {
+            return reinterpret_cast<const f32x4 *>(s_tile[k * NG + group])[(j * MF + i) * kWave + lane];
+        };
+        f32x4 v = part(0);
 #pragma unroll
-        for (int k = 1; k < KS; ++k) v += s_sum[group][k][j][i][lane];
+        for (int k = 1; k < KS; ++k) v += part(k);
         return v;
     };
     constexpr int SHARE = (SETS * MF + KS - 1) / KS;  // results a wave finishes, at most
@@ -579,7 +605,7 @@ __global__ __launch_bounds__(NG *KS *kWave, WAVES) void expert_gemm_narrow_kerne
         for (int o = 0; o < SHARE; ++o) {
             const int u = o * KS + ks, j = u % SETS, i = u / SETS;
             if (u >= SETS * MF) break;
-            const f32x4 g = total(j, i), v = total(2 + j, i);
+            const f32x4 g = total(j, i), v = total(SETS + j, i);
             float top = 0.0f;
 #pragma unroll
             for (int k = 0; k < 4; ++k) {
@@ -622,45 +648,62 @@ struct Plan {
     int threads, rows, cols;
 };
 
-template <bool SWIGLU, int MF, int NG, int KS, int WAVES>
+template <bool SWIGLU, int MF, int WF, int NG, int KS, int DEEP, int WAVES>
 Plan narrow() {
-    return {expert_gemm_narrow_kernel<SWIGLU, MF, NG, KS, WAVES>, NG * KS * kWave, 16 * MF, SWIGLU ? 128 : 64 * NG};
+    return {expert_gemm_narrow_kernel<SWIGLU, MF, WF, NG, KS, DEEP, WAVES>, NG * KS * kWave, 16 * MF,
+            SWIGLU ? 128 : 16 * WF * NG};
 }
 
 // The choice rests on the mean rows of an expert, all that the host knows of the sizes.  Measured
-// over 32 experts, SwiGLU of 7168 channels to 2048 and product of 2048 to 7168, us:
-//   mean rows            4    8   12   16   32   64   96  128  192  256  512
-//   SwiGLU   narrow    177  179  239  236  360
-//            wide 128       187  170  170  172  219  263  405  484  600 1060
-//   product  narrow     85   90  100  114  176
-//            wide 128       104  103  103  105  106  113  146  178  219  387
-//            wide 256                           122  125  137  155  195  335
-// Where there are fewer blocks than compute units a block's own time counts.  One expert, product of
-// 7168 channels to 2048 and of 2048 to 7168, us:
-//   rows                 1   16   64  128  256  512 1024 2048 4096 |   1   64  256 1024 2048 4096
-//   split (32 rows)     19   23   27   27   27   52  101  198  393 |   8   10   36  118  230  460
-//   wide 128                 36   39   59   59   59   59   63   84 |       15   21   23   44   94
-//   wide 256                            96   96   96   96   96  101 |            31   32   38   77
-// and SwiGLU of 7168 to 2048 takes 80 narrow, 57 wide up to 64 rows.
+// over 32 experts, SwiGLU of 7168 channels to 2048 and product of 2048 to 7168, us (s: narrow<...> by
+// its MF, WF, NG and KS):
+//   mean rows               4    8   12   16   24   32   48   64   96  128  192  256  512
+//   SwiGLU   s 1, 4, 4, 2 165  165  194  192  237  262
+//            s 2, 4, 4, 2 170  168  170  172  217  229
+//            wide 128          187  170  170       172       219  263  405  484  600 1060
+//   product  s 1, 4, 1, 8  80   83   88   98  120  134
+//            s 2, 4, 1, 8 105  111  110  113  122  145
+//            s 2, 4, 2, 2  86   91   92   92   96  111  128
+//            wide 128          104  103  103       105       106  113  146  178  219  387
+//            wide 256                                        122  125  137  155  195  335
+// Where there are fewer blocks than compute units a block's own time counts, and more waves of a block
+// on the channels, or fewer columns a block, shorten it.  One expert, product of 7168 channels to 2048
+// and of 2048 to 7168, and SwiGLU of 7168 to 2048, us:
+//   rows                    1   16   64  128  256  512 1024 2048 4096 |   1   64  128  256 1024 2048 4096
+//   product  s 1, 1, 1, 8   6    8   13   24   44                     |   6   20   36
+//            s 1, 4, 1, 8   9   11   11   13   20   34   65           |   6    9   15   24
+//            s 2, 4, 1, 8  11   13   15   15   16   28   54  105      |   7    8   13   25   79
+//            wide 128           36   39   59   59   59   59   63   84 |       15   20   21   23   44   94
+//            wide 256                            96   96   96   96  101 |                 31   32   38   77
+//   SwiGLU   s 1, 4, 4, 2  36   37   37   37   40   79  151
+//            s 2, 4, 4, 2  43   44   47   46   47   52  101  199
+//            wide 128      57   58   58   91   91   92   96  128  237
 constexpr int kComputeUnits = 256;
 Plan plan(const GemmArgs &a) {
     const int64_t mean = a.num_rows / a.num_experts;
+    const int64_t busy = a.num_experts < a.num_rows ? a.num_experts : a.num_rows;
+    // blocks to expect: a segment's last tile is half full on average
+    auto blocks = [&](int rows, int cols) {
+        int64_t tiles = (a.num_rows + busy * rows / 2) / rows;
+        if (a.num_experts == 1) tiles = ((int64_t)a.num_rows + rows - 1) / rows;
+        return (tiles > busy ? tiles : busy) * ((a.n + cols - 1) / cols);
+    };
     if (a.swiglu) {
-        // a block for every compute unit, or the wide kernel's coalesced loads are faster
-        if (mean <= 8 && row_tiles(a, 16) * (a.n / 128) >= kComputeUnits) return narrow<true, 1, 4, 1, 3>();
+        if (mean <= 8 || blocks(16, 128) <= kComputeUnits) return narrow<true, 1, 4, 4, 2, 2, 2>();
+        if (blocks(32, 128) <= kComputeUnits) return narrow<true, 2, 4, 4, 2, 2, 2>();
         return {expert_gemm_wide_kernel<true, 2>, kBlockThreads, 128, 128};
     }
-    if (row_tiles(a, 32) * ((a.n + 63) / 64) <= 2 * kComputeUnits) return narrow<false, 2, 1, 8, 2>();
-    if (mean <= 8) return narrow<false, 1, 2, 2, 3>();
-    // rounds of blocks over the compute units, a round of 256 rows 1.5 times one of 128; a segment's
-    // last tile is half full on average
-    auto rounds = [&](int rows) {
-        const int64_t cols = (a.n + kBN - 1) / kBN;
-        const int64_t halves = a.num_experts == 1 ? 2 * (((int64_t)a.num_rows + rows - 1) / rows)
-                                                  : a.num_experts + 2 * (int64_t)a.num_rows / rows;
-        return (halves * cols + 2 * kComputeUnits - 1) / (2 * kComputeUnits);
+    if (blocks(16, 16) <= kComputeUnits) return narrow<false, 1, 1, 1, 8, 3, 2>();
+    if (mean <= 12 || blocks(16, 64) <= kComputeUnits) return narrow<false, 1, 4, 1, 8, 2, 2>();
+    if (blocks(32, 64) <= 2 * kComputeUnits) return narrow<false, 2, 4, 1, 8, 2, 2>();
+    if (mean <= 24) return narrow<false, 2, 4, 2, 2, 2, 3>();
+    // halves of rounds of blocks over the compute units, whole rounds where there are few; a round of
+    // 256 rows takes 1.5 times one of 128
+    auto time = [&](int rows) {
+        const int64_t all = blocks(rows, kBN), rounds = (all + kComputeUnits - 1) / kComputeUnits;
+        return rounds <= 2 ? rounds * kComputeUnits : all;
     };
-    if (3 * rounds(256) <= 2 * rounds(128)) return {expert_gemm_wide_kernel<false, 4>, kBlockThreads, 256, kBN};
+    if (3 * time(256) <= 2 * time(128)) return {expert_gemm_wide_kernel<false, 4>, kBlockThreads, 256, kBN};
     return {expert_gemm_wide_kernel<false, 2>, kBlockThreads, 128, kBN};
 }
 

@@ -102,10 +102,12 @@ def test_product_many_experts(rows, E):
     assert status == 0
 
 
-# (experts, rows, n, k): every kernel of the product (split channels, few rows of many experts, 128 and 256 rows a
-# block) and of the SwiGLU form (few rows of many experts, 128 rows a block)
+# (experts, rows, n, k): every kernel of the product (16 rows by 16 and 64 columns, 32 rows by 64 and 128, 128 and
+# 256 rows a block) and of the SwiGLU form (16, 32 and 128 rows a block); the last ones give every wave that shares
+# the channels several blocks of them
 KERNELS = [(1, 3, 256, 640), (3, 90, 256, 640), (40, 130, 1024, 384), (70, 100, 2048, 128), (6, 700, 2048, 256),
-           (3, 900, 1024, 128), (2, 1300, 8192, 128), (1, 4400, 2048, 128)]
+           (3, 900, 1024, 128), (2, 1300, 8192, 128), (1, 4400, 2048, 128), (40, 700, 2048, 384),
+           (1, 20, 256, 4096), (2, 40, 2048, 2176), (2, 300, 2048, 2304)]
 
 
 @pytest.mark.parametrize("case", KERNELS, ids=str)
