@@ -9,8 +9,9 @@
 // Choices compare as in binary64 -- a last-bit difference of a 32-bit exp must not decide which of
 // two nearly equal experts a token goes to -- but are formed in f32 first.  With no bias the logits
 // themselves order the experts, and f32 is exact.  Otherwise f32 choices are off by a known part
-// of their size: where two neighbours in the order found, or the last group kept and the best one
-// dropped, are no further apart than that, the wave does the token over in binary64.
+// of their size.  Where two neighbours in the order found are no further apart than that, the order
+// is followed down to a wider step, and the experts above it are ordered anew in binary64; where the
+// last group kept and the best one dropped are, the groups are rated in binary64.
 #include <limits.h>
 
 #include "ep_experts_internal.h"
@@ -117,13 +118,14 @@ __device__ __forceinline__ void wave_lds_order() {
 // NaN and +inf: not a logit (or bias) the router can use.
 __device__ __forceinline__ bool unusable(float v) { return !(v < INFINITY); }
 
-// How far apart two f32 choices have to be for their order to be sure, relative to 1 + their size.
-// With u = 2^-24: an exponential is off by (|argument| + 2) u of it at most, which for the argument
-// l - max of a softmax is under 2 u of 1, and for a sigmoid (whose argument is exact) under 2 u of the
-// score; sum and quotient of a sigmoid add 2 u, the bias u of the choice.  A softmax divides by a sum
-// whose terms are off by the same and whose 38 additions at most by u each: under 60 u.  Twice that
-// for two sides, and half as much again to spare.
-constexpr float kSigmoidSlack = 16 * 0x1p-24f, kSoftmaxSlack = 180 * 0x1p-24f;
+// How far apart two f32 choices have to be for their order to be sure: kSlack of the larger one's size
+// and kSigmoidSlack, or kSoftmaxSlack of the token's largest score.  With u = 2^-24: an exponential is off by
+// (|argument| + 2) u of it at most, which for the argument l - max of a softmax is under 2 u of 1, and
+// for a sigmoid (whose argument is exact) under 2 u of the score; sum and quotient of a sigmoid add
+// 2 u, the bias u of the choice.  A softmax divides by a sum whose terms are off by the same and whose
+// 38 additions at most by u each: under 60 u of the largest score.  Twice that for two sides, and half
+// as much again to spare.
+constexpr float kSlack = 16 * 0x1p-24f, kSigmoidSlack = 16 * 0x1p-24f, kSoftmaxSlack = 180 * 0x1p-24f;
 
 // f32 to an integer that orders as it does (+0 and -0 alike); kNone is below all of them.
 constexpr int kNone = INT_MIN;
@@ -199,7 +201,7 @@ struct Part {
 
 // Which groups stay, as a bit each (a rating orders as `exact` or `rough` does, ties to the lower
 // group), from lane g's rating of group g.  Returns in *close whether a group kept and one dropped
-// are within `slack` of each other.
+// are no further apart than `slack` and twice kSlack of the rating's size.
 template <int LPT, typename F>
 __device__ __forceinline__ uint64_t keep_groups(F rating, int G, int kept, float slack, int lane, bool *close) {
     const int at = lane & (LPT - 1), base = lane & (kWave - LPT);
@@ -222,7 +224,7 @@ __device__ __forceinline__ uint64_t keep_groups(F rating, int G, int kept, float
         for (int g = 0; g < G; ++g) {
             const float o = (float)rating_of(g), r = (float)rating;
             // -inf (a group without experts to choose) is near nothing
-            near |= at < G && ((bits >> g) & 1ull) != (uint64_t)stays && fabsf(o - r) <= slack * (1.0f + fabsf(r));
+            near |= at < G && ((bits >> g) & 1ull) != (uint64_t)stays && fabsf(o - r) <= slack + 2.0f * kSlack * fabsf(r);
         }
         *close = token_bits<LPT>(ballot64(near), lane) != 0ull;
     }
@@ -234,19 +236,122 @@ struct Chosen {
     int expert, key;
 };
 
-// The choice in f32 for the token whose logits start at element `row`.  chosen (LDS): the slots, all
-// without an expert before, and one behind them.  Returns whether some token of the wave needs
-// choose_exact.
+// Experts of a token that may have to be ordered anew: its slots, the one behind them and a few more.
+constexpr int kCandidates = kMaxTopk + 8;
+
+// The lane's choices in binary64 (-inf: not to be chosen).  choice (LDS): VPL values, kWave apart.  The
+// logits go through LDS too, so that the exponentials are a loop: it is seldom run, and there are up to 32.
+template <int LPT, int VPL>
+__device__ __forceinline__ void exact_choices(const RouteParams &p, const Part<VPL> &t, double *choice) {
+    const bool biased = p.a.bias != nullptr;
+    int m = kNone;
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const int o = t.logit[i] > -INFINITY ? order_of(t.logit[i]) : kNone;
+        m = o > m ? o : m;
+        choice[i * kWave] = (double)t.logit[i];
+    }
+    m = token_max<LPT>(m);
+    const double top = m == kNone ? 0.0 : (double)value_of(m);
+    double sum = 0.0;
+#pragma unroll 1
+    for (int i = 0; i < VPL; ++i) {
+        const double l = choice[i * kWave];
+        double c = 0.0;
+        if (l > -INFINITY) c = p.sigmoid ? 1.0 / (1.0 + exp(-l)) : exp(l - top);
+        choice[i * kWave] = c;
+        sum += c;
+    }
+    sum = p.sigmoid ? 1.0 : token_sum<LPT>(sum);
+#pragma unroll
+    for (int i = 0; i < VPL; ++i) {
+        const bool able = t.logit[i] > -INFINITY && t.bias[i] > -INFINITY;
+        const double c = choice[i * kWave] / sum + (biased ? (double)t.bias[i] : 0.0);
+        choice[i * kWave] = able ? c : -INFINITY;
+    }
+}
+
+// Lane g: the rating of group g from choices in binary64.
+template <int LPT, int VPL>
+__device__ __forceinline__ double exact_rating(const RouteParams &p, const double *choice, int lane) {
+    const int at = lane & (LPT - 1), first = at * VPL;
+    const double none = -INFINITY;
+    auto best_two = [&](int lo, int hi, double &a, double &b) {
+        a = b = none;
+#pragma unroll 1
+        for (int i = 0; i < VPL; ++i) {
+            const double v = first + i >= lo && first + i < hi ? choice[i * kWave] : none;
+            b = v > a ? a : v > b ? v : b;
+            a = v > a ? v : a;
+        }
+    };
+    auto join = [&](double &a, double &b, int s) {
+        const double oa = shfl_xor_f64(a, s), ob = shfl_xor_f64(b, s);
+        const double low = a < oa ? a : oa;
+        a = a > oa ? a : oa;
+        b = b > ob ? b : ob;
+        b = b > low ? b : low;
+    };
+    const int lanes = p.group_size / VPL;  // as in choose()
+    double a, b, rating = none;
+    if (p.group_size % VPL == 0 && (lanes & (lanes - 1)) == 0) {
+        const int lo = first / p.group_size * p.group_size;
+        best_two(lo, lo + p.group_size, a, b);
+        for (int s = 1; s < lanes; s <<= 1) join(a, b, s);
+        rating = shfl_f64(p.best == 2 && b > none ? a + b : a, (lane & (kWave - LPT)) + ((at * lanes) & (LPT - 1)));
+        if (at >= p.G) rating = none;
+    } else {
+#pragma unroll 1
+        for (int g = 0; g < p.G; ++g) {
+            best_two(g * p.group_size, (g + 1) * p.group_size, a, b);
+            for (int s = 1; s < LPT; s <<= 1) join(a, b, s);
+            if (at == g) rating = p.best == 2 && b > none ? a + b : a;
+        }
+    }
+    return rating;
+}
+
+// The num_topk largest choices in binary64, one after the other: where more experts are near each other
+// than there are candidates.
+template <int LPT, int VPL>
+__device__ __forceinline__ void choose_exact(const RouteParams &p, int lane, double *choice, Chosen *chosen) {
+    const int at = lane & (LPT - 1);
+    const double none = -INFINITY;
+#pragma unroll 1
+    for (int j = 0; j < p.K; ++j) {
+        double m = none;
+        int e = 0;
+#pragma unroll 1
+        for (int i = 0; i < VPL; ++i) {
+            const double v = choice[i * kWave];
+            if (v > m) {
+                m = v;
+                e = i;
+            }
+        }
+        const double best = token_max<LPT>(m);
+        const uint64_t holders = token_bits<LPT>(ballot64(m == best && best > none), lane);
+        if (holders == 0ull) {
+            if (at == 0) chosen[j].expert = -1;
+        } else if (at == __builtin_ctzll(holders)) {
+            choice[e * kWave] = none;
+            chosen[j].expert = at * VPL + e;
+        }
+    }
+}
+
+// The choice for the token whose logits start at element `row`.  chosen (LDS): its candidates, all
+// without an expert before; the first num_topk are the choice.  value (LDS): a number for each.  exact
+// (LDS): the wave's, VPL x kWave.
 template <int LPT, int VPL, bool BF16>
-__device__ __forceinline__ bool choose(const RouteParams &p, const Part<VPL> &t, int64_t row, int lane,
-                                       Chosen *chosen) {
+__device__ __forceinline__ void choose(const RouteParams &p, const Part<VPL> &t, int64_t row, int lane,
+                                       double (*exact)[kWave], Chosen *chosen, double *value) {
     const int at = lane & (LPT - 1);
     const bool biased = p.a.bias != nullptr;
     const bool by_logit = !biased && p.best == 1;  // what rates a group
-    const float slack = p.sigmoid ? kSigmoidSlack : kSoftmaxSlack;
+    float slack = kSigmoidSlack;
     float choice[VPL];
     int key[VPL];
-    bool close = false;
     if (biased || (p.G > 1 && !by_logit)) {
         float top = 0.0f, sum = 1.0f;
         if (!p.sigmoid) {
@@ -266,7 +371,10 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const Part<VPL> &t,
             sum += choice[i];
         }
         float scale = 1.0f;
-        if (!p.sigmoid) scale = 1.0f / token_sum<LPT>(sum);
+        if (!p.sigmoid) {
+            scale = 1.0f / token_sum<LPT>(sum);  // the largest score
+            slack = kSoftmaxSlack * fminf(scale, 1.0f);
+        }
 #pragma unroll
         for (int i = 0; i < VPL; ++i) choice[i] = __builtin_fmaf(choice[i], scale, biased ? t.bias[i] : 0.0f);
     }
@@ -275,6 +383,8 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const Part<VPL> &t,
         const bool able = t.logit[i] > -INFINITY && (!biased || t.bias[i] > -INFINITY);
         key[i] = able ? order_of(biased ? choice[i] : t.logit[i]) : kNone;
     }
+    uint64_t keep = ~0ull;
+    bool have_exact = false;
     if (p.G > 1) {
         float rating = -INFINITY;  // lane g: of group g
         auto best_two = [&](int lo, int hi, int &a, int &b) {
@@ -288,12 +398,6 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const Part<VPL> &t,
                 b = low > b ? low : b;
             }
         };
-        auto join = [&](int &a, int &b, int oa, int ob) {
-            const int low = a < oa ? a : oa;
-            a = a > oa ? a : oa;
-            b = b > ob ? b : ob;
-            b = b > low ? b : low;
-        };
         auto rate = [&](int a, int b) {
             if (a == kNone) return -INFINITY;
             return p.best == 2 && b != kNone ? value_of(a) + value_of(b) : value_of(a);
@@ -303,7 +407,12 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const Part<VPL> &t,
             const int lo = t.first / p.group_size * p.group_size;
             int a, b;
             best_two(lo, lo + p.group_size, a, b);
-            for (int s = 1; s < lanes; s <<= 1) join(a, b, __shfl_xor(a, s), __shfl_xor(b, s));
+            for (int s = 1; s < lanes; s <<= 1) {
+                const int oa = __shfl_xor(a, s), ob = __shfl_xor(b, s), low = a < oa ? a : oa;
+                a = a > oa ? a : oa;
+                b = b > ob ? b : ob;
+                b = b > low ? b : low;
+            }
             rating = rate(a, b);
             const int from = at * lanes;  // a lane of group `at`
             rating = __shfl(rating, (lane & (kWave - LPT)) + (from & (LPT - 1)));
@@ -312,25 +421,39 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const Part<VPL> &t,
             for (int g = 0; g < p.G; ++g) {
                 int a, b;
                 best_two(g * p.group_size, (g + 1) * p.group_size, a, b);
-                for (int s = 1; s < LPT; s <<= 1) join(a, b, __shfl_xor(a, s), __shfl_xor(b, s));
-                if (at == g) rating = rate(a, b);
+                const int most = token_max<LPT>(a);
+                int second = kNone;
+                if (p.best == 2) {  // the second of a lane that holds the first, or the first of another
+                    const uint64_t holders = token_bits<LPT>(ballot64(a == most), lane);
+                    second = token_max<LPT>(at == __builtin_ctzll(holders) ? b : a);
+                }
+                if (at == g) rating = rate(most, second);
             }
         }
-        const uint64_t keep = keep_groups<LPT>(rating, p.G, p.kept, 2.0f * slack, lane, by_logit ? nullptr : &close);
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            const int g = (t.first + i) / p.group_size;
-            if (g >= p.G || ((keep >> g) & 1ull) == 0ull) key[i] = kNone;
+        bool close = false;
+        keep = keep_groups<LPT>(rating, p.G, p.kept, 2.0f * slack, lane, by_logit ? nullptr : &close);
+        if (ballot64(close) != 0ull) {
+            exact_choices<LPT, VPL>(p, t, &exact[0][lane]);
+            have_exact = true;
+            keep = keep_groups<LPT>(exact_rating<LPT, VPL>(p, &exact[0][lane], lane), p.G, p.kept, 0.0f, lane, nullptr);
         }
     }
-    // num_topk rounds: the largest key left, lowest expert first; and one more, to see how near it is
-    const int rounds = p.K + (biased ? 1 : 0);
-    for (int j = 0; j < rounds; ++j) {
+    auto kept = [&](int e) {
+        const int g = e / p.group_size;
+        return g < p.G && ((keep >> g) & 1ull) != 0ull;
+    };
+    if (p.G > 1) {
+#pragma unroll
+        for (int i = 0; i < VPL; ++i)
+            if (!kept(t.first + i)) key[i] = kNone;
+    }
+    // a round: the largest key left, lowest expert first
+    auto round = [&](int j) {
         int m = key[0];
 #pragma unroll
         for (int i = 1; i < VPL; ++i) m = key[i] > m ? key[i] : m;
         const int best = token_max<LPT>(m);
-        if (ballot64(best != kNone) == 0ull) break;
+        if (ballot64(best != kNone) == 0ull) return false;
         const uint64_t holders = token_bits<LPT>(ballot64(m == best && best != kNone), lane);
         const bool mine = holders != 0ull && at == __builtin_ctzll(holders | (1ull << 63));
         int e = 0;
@@ -343,131 +466,88 @@ __device__ __forceinline__ bool choose(const RouteParams &p, const Part<VPL> &t,
             done |= hit;
         }
         if (mine) chosen[j] = {t.first + e, best};
-    }
-    if (biased) {
-        // lane j: slots j and j + 1.  The same logit and bias are a tie in any precision
-        wave_lds_order();
-        for (int j = at; j < p.K; j += LPT) {
-            const Chosen a = chosen[j], b = chosen[j + 1];
-            if (b.expert < 0) continue;
-            const float v = value_of(a.key);
-            if (v - value_of(b.key) > slack * (1.0f + fabsf(v))) continue;
-            close |= load_logit<BF16>(p.a.logits, row + a.expert) != load_logit<BF16>(p.a.logits, row + b.expert) ||
-                     p.a.bias[a.expert] != p.a.bias[b.expert];
-        }
-    }
-    return ballot64(close) != 0ull;
-}
-
-// The same in binary64 throughout, for waves with near ties: few, so it is written to take few
-// registers.  choice (LDS): the lane's VPL values, kWave apart.  on: the token is routed.
-template <int LPT, int VPL, bool BF16>
-__device__ __forceinline__ void choose_exact(const RouteParams &p, int64_t row, bool on, int lane, double *choice,
-                                             Chosen *chosen) {
-    const int at = lane & (LPT - 1), first = at * VPL;
-    const bool biased = p.a.bias != nullptr;
-    const double none = -INFINITY;
-    auto logit_of = [&](int i) {
-        if (!on || first + i >= p.E) return -INFINITY;
-        const float l = load_logit<BF16>(p.a.logits, row + first + i);
-        return unusable(l) ? -INFINITY : l;
+        return true;
     };
-    float top = -INFINITY;
-#pragma unroll 1
-    for (int i = 0; i < VPL; ++i) top = fmaxf(top, logit_of(i));
-    for (int s = 1; s < LPT; s <<= 1) top = fmaxf(top, __shfl_xor(top, s));
-    double sum = 0.0;
-#pragma unroll 1
-    for (int i = 0; i < VPL; ++i) {
-        const float l = logit_of(i);
-        double c = 0.0;
-        if (l > -INFINITY) c = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)top);
-        choice[i * kWave] = c;
-        sum += c;
+    // num_topk rounds, and with a bias one more, to see how near it is
+    const int rounds = p.K + (biased ? 1 : 0);
+    for (int j = 0; j < rounds; ++j)
+        if (!round(j)) break;
+    wave_lds_order();
+    if (!biased) return;
+
+    auto near = [&](const Chosen &a, const Chosen &b) {
+        const float v = value_of(a.key);
+        return b.expert >= 0 && v - value_of(b.key) <= slack + kSlack * fabsf(v);
+    };
+    // Lane j: slots j and j + 1.  The same logit and bias are a tie in any precision; but those behind
+    // the last slot may be followed by others that are not the same.
+    bool close = false;
+    for (int j = at; j < p.K; j += LPT) {
+        const Chosen a = chosen[j], b = chosen[j + 1];
+        if (near(a, b))
+            close |= j + 1 == p.K || load_logit<BF16>(p.a.logits, row + a.expert) != load_logit<BF16>(p.a.logits, row + b.expert) ||
+                     p.a.bias[a.expert] != p.a.bias[b.expert];
     }
-    sum = p.sigmoid ? 1.0 : token_sum<LPT>(sum);
-#pragma unroll 1
-    for (int i = 0; i < VPL; ++i) {
-        double c = choice[i * kWave] / sum;
-        bool able = logit_of(i) > -INFINITY;
-        if (biased && able) {
-            const float b = p.a.bias[first + i];
-            able = b > -INFINITY && !unusable(b);
-            c += (double)b;
-        }
-        choice[i * kWave] = able ? c : none;
+    if (ballot64(close) == 0ull) return;
+    int n = p.K + 1;
+    bool open = near(chosen[n - 2], chosen[n - 1]);
+    while (n < kCandidates && ballot64(open) != 0ull) {
+        if (!round(n)) open = false;
+        wave_lds_order();
+        ++n;
+        open = open && near(chosen[n - 2], chosen[n - 1]);
     }
-    if (p.G > 1) {
-        double rating = none;
-        auto best_two = [&](int lo, int hi, double &a, double &b) {
-            a = b = none;
-#pragma unroll 1
-            for (int i = 0; i < VPL; ++i) {
-                const double v = first + i >= lo && first + i < hi ? choice[i * kWave] : none;
-                b = v > a ? a : v > b ? v : b;
-                a = v > a ? v : a;
-            }
-        };
-        auto join = [&](double &a, double &b, int s) {
-            const double oa = shfl_xor_f64(a, s), ob = shfl_xor_f64(b, s);
-            const double low = a < oa ? a : oa;
-            a = a > oa ? a : oa;
-            b = b > ob ? b : ob;
-            b = b > low ? b : low;
-        };
-        const int lanes = p.group_size / VPL;  // as in choose()
-        double a, b;
-        if (p.group_size % VPL == 0 && (lanes & (lanes - 1)) == 0) {
-            const int lo = first / p.group_size * p.group_size;
-            best_two(lo, lo + p.group_size, a, b);
-            for (int s = 1; s < lanes; s <<= 1) join(a, b, s);
-            rating = shfl_f64(p.best == 2 && b > none ? a + b : a, (lane & (kWave - LPT)) + ((at * lanes) & (LPT - 1)));
-            if (at >= p.G) rating = none;
-        } else {
-#pragma unroll 1
-            for (int g = 0; g < p.G; ++g) {
-                best_two(g * p.group_size, (g + 1) * p.group_size, a, b);
-                for (int s = 1; s < LPT; s <<= 1) join(a, b, s);
-                if (at == g) rating = p.best == 2 && b > none ? a + b : a;
-            }
-        }
-        const uint64_t keep = keep_groups<LPT>(rating, p.G, p.kept, 0.0f, lane, nullptr);
-#pragma unroll 1
-        for (int i = 0; i < VPL; ++i) {
-            const int g = (first + i) / p.group_size;
-            if (g >= p.G || ((keep >> g) & 1ull) == 0ull) choice[i * kWave] = none;
-        }
+    const bool overflow = ballot64(open) != 0ull;
+    if ((overflow || !p.sigmoid) && !have_exact) {
+        exact_choices<LPT, VPL>(p, t, &exact[0][lane]);
+        have_exact = true;
     }
-    if (!biased) {
+    wave_lds_order();
+    if (overflow) {
 #pragma unroll 1
         for (int i = 0; i < VPL; ++i)
-            if (choice[i * kWave] > none) choice[i * kWave] = (double)logit_of(i);
+            if (!kept(t.first + i)) exact[i][lane] = -INFINITY;
+        choose_exact<LPT, VPL>(p, lane, &exact[0][lane], chosen);
+        return;
     }
-#pragma unroll 1
-    for (int j = 0; j < p.K; ++j) {
-        double m = none;
-        int e = 0;
-#pragma unroll 1
-        for (int i = 0; i < VPL; ++i) {
-            const double v = choice[i * kWave];
-            if (v > m) {
-                m = v;
-                e = i;
-            }
-        }
-        const double best = token_max<LPT>(m);
-        const uint64_t holders = token_bits<LPT>(ballot64(m == best && best > none), lane);
-        if (holders != 0ull && at == __builtin_ctzll(holders | (1ull << 63))) {
-            choice[e * kWave] = none;
-            chosen[j].expert = first + e;
-        }
+    constexpr int kMine = (kCandidates + LPT - 1) / LPT;  // a lane's candidates
+    int place[kMine], expert[kMine];
+    for (int j = at; j < n; j += LPT) {
+        const int e = chosen[j].expert;
+        double v = -INFINITY;
+        if (e >= 0 && have_exact)
+            v = exact[e % VPL][(lane & (kWave - LPT)) + e / VPL];
+        else if (e >= 0)
+            v = 1.0 / (1.0 + exp(-(double)load_logit<BF16>(p.a.logits, row + e))) + (double)p.a.bias[e];
+        value[j] = v;
     }
+    wave_lds_order();
+#pragma unroll
+    for (int u = 0; u < kMine; ++u) {
+        const int j = at + u * LPT;
+        expert[u] = -1;
+        place[u] = p.K;
+        if (j >= n || chosen[j].expert < 0) continue;
+        const double v = value[j];
+        int ahead = 0;
+        expert[u] = chosen[j].expert;
+        for (int o = 0; o < n; ++o) {
+            const int e = chosen[o].expert;
+            ahead += e >= 0 && (value[o] > v || (value[o] == v && e < expert[u]));
+        }
+        place[u] = ahead;
+    }
+    wave_lds_order();
+#pragma unroll
+    for (int u = 0; u < kMine; ++u)
+        if (place[u] < p.K) chosen[place[u]].expert = expert[u];
 }
 
 template <int LPT, int VPL, bool BF16>
 __global__ __launch_bounds__(kRouteWaves *kWave) void route_kernel(RouteParams p) {
     constexpr int kTokens = kWave / LPT;  // of a wave
-    __shared__ Chosen s_chosen[kRouteWaves * kTokens][kMaxTopk + 1];
+    __shared__ Chosen s_chosen[kRouteWaves * kTokens][kCandidates];
+    __shared__ double s_value[kRouteWaves * kTokens][kCandidates];
     __shared__ double s_exact[kRouteWaves][VPL][kWave];
     const int lane = threadIdx.x & (kWave - 1), at = lane & (LPT - 1);
     const int slot = threadIdx.x / LPT;  // the token's place in the block
@@ -507,16 +587,9 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_kernel(RouteParams p
     }
     if (ballot64(bad) != 0ull && lane == 0) flag(p.a.dev_status, EP_DEV_BAD_LOGIT);
 
-    auto clear = [&] {
-        for (int j = at; j <= p.K; j += LPT) s_chosen[slot][j] = {-1, kNone};
-        wave_lds_order();
-    };
-    clear();
-    if (choose<LPT, VPL, BF16>(p, part, row, lane, s_chosen[slot])) {
-        wave_lds_order();
-        clear();
-        choose_exact<LPT, VPL, BF16>(p, row, on, lane, &s_exact[threadIdx.x / kWave][0][lane], s_chosen[slot]);
-    }
+    for (int j = at; j < kCandidates; j += LPT) s_chosen[slot][j] = {-1, kNone};
+    wave_lds_order();
+    choose<LPT, VPL, BF16>(p, part, row, lane, s_exact[threadIdx.x / kWave], s_chosen[slot], s_value[slot]);
     wave_lds_order();
 
     // lane j: slot j (num_topk <= LPT, which the launcher sees to).  In 64 bits: there are few of them

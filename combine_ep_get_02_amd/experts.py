@@ -64,7 +64,7 @@ _LOGITS = {torch.float32: EP_LOGITS_F32, torch.bfloat16: EP_LOGITS_BF16}
 
 def _device() -> int:
     """The current GPU; none before the first use of one, when no tensor can be on it."""
-    return torch.cuda.current_device() if torch.cuda.is_initialized() else -2
+    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
 
 
 def _raw_stream(stream, device) -> int | None:

@@ -109,6 +109,56 @@ def test_near_ties_among_many_and_few_tokens(T, kind):
         _weights_near(got_w[at], want_w, kind, True)
 
 
+@pytest.mark.parametrize("T", [500, 2100])
+@pytest.mark.parametrize("kind", sorted(KINDS))
+@pytest.mark.parametrize("k", [1, 2, 3])
+def test_near_tie_behind_equal_experts(T, kind, k):
+    """Experts 5 and 9 are equal and fill the last slot and the one behind it; expert 2 is a hair above or below."""
+    rng = np.random.default_rng(T + k)
+    E = 64
+    values = np.full((T, E), -6.0, np.float32)
+    bias = np.zeros(E, np.float32)
+    bias[2] = 0.1
+    s = 0.2 + 0.1 * rng.random(T)  # of experts 5 and 9; the others' scores are far below
+    if kind == "sigmoid":
+        values[:, 5] = values[:, 9] = np.log(s / (1 - s))
+        v5 = 1 / (1 + np.exp(-values[:, 5].astype(np.float64)))
+        values[:, 2] = np.log((v5 - 0.1) / (1.1 - v5))
+    else:
+        # scores p5 = p9 = s and p2 = s - bias, the rest shared out
+        rest = (1 - 3 * s + float(bias[2])) / (E - 3)
+        values[:] = np.log(rest)[:, None]
+        values[:, 5] = values[:, 9] = np.log(s)
+        values[:, 2] = np.log(s - float(bias[2]))
+    steps = rng.integers(-2, 3, size=T)
+    for _ in range(2):  # a step or two of f32 either way
+        values[:, 2] = np.where(steps > 0, np.nextafter(values[:, 2], np.float32(9)),
+                                np.where(steps < 0, np.nextafter(values[:, 2], np.float32(-99)), values[:, 2]))
+        steps -= np.sign(steps)
+    got_i, _, _ = _route(torch.from_numpy(values).cuda(), torch.from_numpy(bias).cuda(), kind, k)
+    want_i, _ = oracle64.route(values, bias, kind, k, 1, 1, 1, True, 1.0)
+    assert len(np.unique(want_i[:, 0])) > 1  # both orders occur
+    assert np.array_equal(got_i, want_i)
+
+
+@pytest.mark.parametrize("T,E,k", [(130, 200, 8), (130, 200, 32), (2100, 200, 16), (2100, 60, 3), (40, 1500, 8)])
+@pytest.mark.parametrize("kind", sorted(KINDS))
+@pytest.mark.parametrize("groups,kept,best", [(1, 1, 1), (10, 4, 2), (20, 7, 1)])
+def test_more_near_ties_than_candidates(T, E, k, kind, groups, kept, best):
+    """Every expert of a token is within a few steps of f32 of every other, or of a part of them."""
+    rng = np.random.default_rng(E + k)
+    base = rng.standard_normal(E).astype(np.float32)
+    values = np.repeat(base[None], T, 0) + (rng.integers(-3, 4, size=(T, E)) * 2.0 ** -23).astype(np.float32)
+    values = values.astype(np.float32)
+    bias = (0.7 - oracle64.scores(base[None], kind)[0]).astype(np.float32)
+    bias[rng.random(E) < 0.5] -= np.float32(0.25)
+    at = np.unique(np.concatenate([np.arange(30), rng.integers(0, T, 30)]))
+    got_i, got_w, _ = _route(torch.from_numpy(values).cuda(), torch.from_numpy(bias).cuda(), kind, k, groups, kept, best)
+    want_i, want_w = oracle64.route(values[at], bias, kind, k, groups, kept, best, True, 1.0)
+    assert np.array_equal(got_i[at], want_i)
+    _weights_near(got_w[at], want_w, kind, True)
+
+
 @pytest.mark.parametrize("E,groups,kept", [(256, 8, 4), (64, 64, 9), (160, 8, 3), (12, 4, 4), (96, 2, 1), (1024, 16, 1)])
 @pytest.mark.parametrize("best", [1, 2])
 @pytest.mark.parametrize("kind", sorted(KINDS))
