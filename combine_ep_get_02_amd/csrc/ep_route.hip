@@ -26,6 +26,7 @@ struct RouteParams {
     RouteArgs a;
     int64_t T;
     int E, K, G, kept, best, group_size;
+    int group_lanes;  // lanes of a token that share a group: a power of two, of all lanes over G
     bool sigmoid, renorm, vector;
     float scale;
 };
@@ -271,44 +272,39 @@ __device__ __forceinline__ void exact_choices(const RouteParams &p, const Part<V
     }
 }
 
-// Lane g: the rating of group g from choices in binary64.
-template <int LPT, int VPL>
-__device__ __forceinline__ double exact_rating(const RouteParams &p, const double *choice, int lane) {
-    const int at = lane & (LPT - 1), first = at * VPL;
-    const double none = -INFINITY;
-    auto best_two = [&](int lo, int hi, double &a, double &b) {
-        a = b = none;
-#pragma unroll 1
-        for (int i = 0; i < VPL; ++i) {
-            const double v = first + i >= lo && first + i < hi ? choice[i * kWave] : none;
-            b = v > a ? a : v > b ? v : b;
+// Lane g: the rating of group g (-inf without experts), from the token's choices in LDS (those of the
+// wave's lane l from choice[l], kWave apart).  group_lanes lanes share a group's experts.
+template <int LPT, int VPL, typename V>
+__device__ __forceinline__ V rate_groups(const RouteParams &p, const V *choice, int lane) {
+    const int at = lane & (LPT - 1), base = lane & (kWave - LPT);
+    const V none = -INFINITY;
+    const int g = at / p.group_lanes;
+    V a = none, b = none;
+    if (g < p.G) {
+        const int end = (g + 1) * p.group_size;
+        for (int e = g * p.group_size + at % p.group_lanes; e < end; e += p.group_lanes) {
+            const V v = choice[e % VPL * kWave + base + e / VPL];
+            const V low = v < a ? v : a;
             a = v > a ? v : a;
+            b = low > b ? low : b;
         }
+    }
+    auto other = [](V v, int s) {
+        if constexpr (sizeof(V) == 8) return shfl_xor_f64(v, s);
+        else return __shfl_xor(v, s);
     };
-    auto join = [&](double &a, double &b, int s) {
-        const double oa = shfl_xor_f64(a, s), ob = shfl_xor_f64(b, s);
-        const double low = a < oa ? a : oa;
+    for (int s = 1; s < p.group_lanes; s <<= 1) {
+        const V oa = other(a, s), ob = other(b, s), low = a < oa ? a : oa;
         a = a > oa ? a : oa;
         b = b > ob ? b : ob;
         b = b > low ? b : low;
-    };
-    const int lanes = p.group_size / VPL;  // as in choose()
-    double a, b, rating = none;
-    if (p.group_size % VPL == 0 && (lanes & (lanes - 1)) == 0) {
-        const int lo = first / p.group_size * p.group_size;
-        best_two(lo, lo + p.group_size, a, b);
-        for (int s = 1; s < lanes; s <<= 1) join(a, b, s);
-        rating = shfl_f64(p.best == 2 && b > none ? a + b : a, (lane & (kWave - LPT)) + ((at * lanes) & (LPT - 1)));
-        if (at >= p.G) rating = none;
-    } else {
-#pragma unroll 1
-        for (int g = 0; g < p.G; ++g) {
-            best_two(g * p.group_size, (g + 1) * p.group_size, a, b);
-            for (int s = 1; s < LPT; s <<= 1) join(a, b, s);
-            if (at == g) rating = p.best == 2 && b > none ? a + b : a;
-        }
     }
-    return rating;
+    const V rating = p.best == 2 && b > none ? a + b : a;
+    const int from = base + ((at * p.group_lanes) & (LPT - 1));
+    V r;
+    if constexpr (sizeof(V) == 8) r = shfl_f64(rating, from);
+    else r = __shfl(rating, from);
+    return at < p.G ? r : none;
 }
 
 // The num_topk largest choices in binary64, one after the other: where more experts are near each other
@@ -386,56 +382,21 @@ __device__ __forceinline__ void choose(const RouteParams &p, const Part<VPL> &t,
     uint64_t keep = ~0ull;
     bool have_exact = false;
     if (p.G > 1) {
-        float rating = -INFINITY;  // lane g: of group g
-        auto best_two = [&](int lo, int hi, int &a, int &b) {
-            a = b = kNone;
+        float *rough = reinterpret_cast<float *>(&exact[0][0]);
 #pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                const int e = t.first + i;
-                const int v = e >= lo && e < hi && key[i] != kNone ? order_of(by_logit ? t.logit[i] : choice[i]) : kNone;
-                const int low = v < a ? v : a;
-                a = v > a ? v : a;
-                b = low > b ? low : b;
-            }
-        };
-        auto rate = [&](int a, int b) {
-            if (a == kNone) return -INFINITY;
-            return p.best == 2 && b != kNone ? value_of(a) + value_of(b) : value_of(a);
-        };
-        const int lanes = p.group_size / VPL;  // lanes that share a group, where groups are whole lanes
-        if (p.group_size % VPL == 0 && (lanes & (lanes - 1)) == 0) {
-            const int lo = t.first / p.group_size * p.group_size;
-            int a, b;
-            best_two(lo, lo + p.group_size, a, b);
-            for (int s = 1; s < lanes; s <<= 1) {
-                const int oa = __shfl_xor(a, s), ob = __shfl_xor(b, s), low = a < oa ? a : oa;
-                a = a > oa ? a : oa;
-                b = b > ob ? b : ob;
-                b = b > low ? b : low;
-            }
-            rating = rate(a, b);
-            const int from = at * lanes;  // a lane of group `at`
-            rating = __shfl(rating, (lane & (kWave - LPT)) + (from & (LPT - 1)));
-            if (at >= p.G) rating = -INFINITY;
-        } else {
-            for (int g = 0; g < p.G; ++g) {
-                int a, b;
-                best_two(g * p.group_size, (g + 1) * p.group_size, a, b);
-                const int most = token_max<LPT>(a);
-                int second = kNone;
-                if (p.best == 2) {  // the second of a lane that holds the first, or the first of another
-                    const uint64_t holders = token_bits<LPT>(ballot64(a == most), lane);
-                    second = token_max<LPT>(at == __builtin_ctzll(holders) ? b : a);
-                }
-                if (at == g) rating = rate(most, second);
-            }
-        }
+        for (int i = 0; i < VPL; ++i)
+            rough[i * kWave + lane] = key[i] == kNone ? -INFINITY : by_logit ? t.logit[i] : choice[i];
+        wave_lds_order();
+        const float rating = rate_groups<LPT, VPL>(p, rough, lane);
+        wave_lds_order();
         bool close = false;
         keep = keep_groups<LPT>(rating, p.G, p.kept, 2.0f * slack, lane, by_logit ? nullptr : &close);
         if (ballot64(close) != 0ull) {
             exact_choices<LPT, VPL>(p, t, &exact[0][lane]);
             have_exact = true;
-            keep = keep_groups<LPT>(exact_rating<LPT, VPL>(p, &exact[0][lane], lane), p.G, p.kept, 0.0f, lane, nullptr);
+            wave_lds_order();
+            const double sure = rate_groups<LPT, VPL>(p, &exact[0][0], lane);
+            keep = keep_groups<LPT>(sure, p.G, p.kept, 0.0f, lane, nullptr);
         }
     }
     auto kept = [&](int e) {
@@ -763,6 +724,8 @@ template <int LPT, int VPL, bool BF16>
 hipError_t start(RouteParams p, hipStream_t stream) {
     constexpr int kTokens = kRouteWaves * kWave / LPT;
     p.vector = whole_words<VPL, BF16>(p.a.logits, p.a.stride, p.E);
+    p.group_lanes = 1;
+    while (2 * p.group_lanes * p.G <= LPT) p.group_lanes *= 2;
     hipLaunchKernelGGL((route_kernel<LPT, VPL, BF16>), dim3((unsigned)((p.T + kTokens - 1) / kTokens)),
                        dim3(kRouteWaves * kWave), 0, stream, p);
     return hipGetLastError();
