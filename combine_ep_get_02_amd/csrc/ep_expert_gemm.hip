@@ -150,7 +150,7 @@ __global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(Gemm
     // wave's last load of a step is of scales: rows' by the first BM lanes, the weights' two by the
     // lanes of the next wave (the others repeat those).  (One array a buffer: the compiler tells them
     // apart, and would wait for all loads before a read of an array that it does not.)
-    constexpr int STAGES = MI == 2 ? 3 : 2;
+    constexpr int STAGES = MI == 4 ? 2 : 3;
     constexpr int kLoads = XL + WL + 1;  // of a wave and step
     static_assert(BM <= 64 * (WM * WN - 1), "a wave is left for the weights' scales");
     constexpr int kX = 0, kW = BM * kUnits, kS = kW + kBN * kUnits, kBuffer = kS + kBlockThreads / 4;
@@ -660,6 +660,7 @@ Plan narrow() {
 //   mean rows               4    8   12   16   24   32   48   64   96  128  192  256  512
 //   SwiGLU   s 1, 4, 4, 2 165  165  194  192  237  262
 //            s 2, 4, 4, 2 170  168  170  172  217  229
+//            wide 64           162  162  163  166  169  173  233  303  399  525  677 1241
 //            wide 128          187  170  170       172       219  263  405  484  600 1060
 //   product  s 1, 4, 1, 8  80   83   88   98  120  134
 //            s 2, 4, 1, 8 105  111  110  113  122  145
@@ -677,6 +678,7 @@ Plan narrow() {
 //            wide 256                            96   96   96   96  101 |                 31   32   38   77
 //   SwiGLU   s 1, 4, 4, 2  36   37   37   37   40   79  151
 //            s 2, 4, 4, 2  43   44   47   46   47   52  101  199
+//            wide 64       38   39   59   59   60   61   72  142  287
 //            wide 128      57   58   58   91   91   92   96  128  237
 constexpr int kComputeUnits = 256;
 Plan plan(const GemmArgs &a) {
@@ -691,6 +693,8 @@ Plan plan(const GemmArgs &a) {
     if (a.swiglu) {
         if (mean <= 8 || blocks(16, 128) <= kComputeUnits) return narrow<true, 1, 4, 4, 2, 2, 2>();
         if (blocks(32, 128) <= kComputeUnits) return narrow<true, 2, 4, 4, 2, 2, 2>();
+        if (mean <= 32 || blocks(64, 128) <= kComputeUnits)
+            return {expert_gemm_wide_kernel<true, 1>, kBlockThreads, 64, 128};
         return {expert_gemm_wide_kernel<true, 2>, kBlockThreads, 128, 128};
     }
     if (blocks(16, 16) <= kComputeUnits) return narrow<false, 1, 1, 1, 8, 3, 2>();

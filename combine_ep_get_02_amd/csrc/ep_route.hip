@@ -45,12 +45,6 @@ __device__ __forceinline__ float load_logit(const void *p, int64_t i) {
     return static_cast<const float *>(p)[i];
 }
 
-__device__ __forceinline__ double shfl_xor_f64(double v, int s) {
-    const uint64_t u = __builtin_bit_cast(uint64_t, v);
-    const uint32_t lo = __shfl_xor((int)(uint32_t)u, s), hi = __shfl_xor((int)(uint32_t)(u >> 32), s);
-    return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
-}
-
 __device__ __forceinline__ double shfl_f64(double v, int from) {
     const uint64_t u = __builtin_bit_cast(uint64_t, v);
     const uint32_t lo = __shfl((int)(uint32_t)u, from), hi = __shfl((int)(uint32_t)(u >> 32), from);
@@ -163,14 +157,29 @@ __device__ __forceinline__ int token_max(int v) {
     }
 }
 
-template <int LPT>
-__device__ __forceinline__ float token_sum(float v) {
-    for (int s = 1; s < LPT; s <<= 1) v += __shfl_xor(v, s);
-    return v;
+// v of lane ^ S, for S below 16 without a trip through LDS.
+template <int S>
+__device__ __forceinline__ float of_lane_xor(float v) {
+    return __uint_as_float(lane_xor<S>(__float_as_uint(v)));
 }
-template <int LPT>
-__device__ __forceinline__ double token_sum(double v) {
-    for (int s = 1; s < LPT; s <<= 1) v += shfl_xor_f64(v, s);
+template <int S>
+__device__ __forceinline__ double of_lane_xor(double v) {
+    const uint64_t u = __builtin_bit_cast(uint64_t, v);
+    return __builtin_bit_cast(double, ((uint64_t)lane_xor<S>((uint32_t)(u >> 32)) << 32) | lane_xor<S>((uint32_t)u));
+}
+__device__ __forceinline__ float of_lane(float v, int l) { return readlanef(v, l); }
+__device__ __forceinline__ double of_lane(double v, int l) {
+    return __builtin_bit_cast(double, readlane64(__builtin_bit_cast(uint64_t, v), l));
+}
+
+// Sum over a token's lanes, in one order for all of them.
+template <int LPT, typename F>
+__device__ __forceinline__ F token_sum(F v) {
+    v += of_lane_xor<1>(v);
+    v += of_lane_xor<2>(v);
+    v += of_lane_xor<4>(v);
+    v += of_lane_xor<8>(v);
+    if constexpr (LPT == kWave) v = (of_lane(v, 0) + of_lane(v, 16)) + (of_lane(v, 32) + of_lane(v, 48));
     return v;
 }
 // The same for doubles, ordered as 64-bit integers in two halves: the largest high half, then the
@@ -282,6 +291,7 @@ __device__ __forceinline__ V rate_groups(const RouteParams &p, const V *choice, 
     V a = none, b = none;
     if (g < p.G) {
         const int end = (g + 1) * p.group_size;
+#pragma unroll 4
         for (int e = g * p.group_size + at % p.group_lanes; e < end; e += p.group_lanes) {
             const V v = choice[e % VPL * kWave + base + e / VPL];
             const V low = v < a ? v : a;
@@ -289,16 +299,17 @@ __device__ __forceinline__ V rate_groups(const RouteParams &p, const V *choice, 
             b = low > b ? low : b;
         }
     }
-    auto other = [](V v, int s) {
-        if constexpr (sizeof(V) == 8) return shfl_xor_f64(v, s);
-        else return __shfl_xor(v, s);
-    };
-    for (int s = 1; s < p.group_lanes; s <<= 1) {
-        const V oa = other(a, s), ob = other(b, s), low = a < oa ? a : oa;
+    auto join = [&](V oa, V ob) {
+        const V low = a < oa ? a : oa;
         a = a > oa ? a : oa;
         b = b > ob ? b : ob;
         b = b > low ? b : low;
-    }
+    };
+    if (p.group_lanes > 1) join(of_lane_xor<1>(a), of_lane_xor<1>(b));
+    if (p.group_lanes > 2) join(of_lane_xor<2>(a), of_lane_xor<2>(b));
+    if (p.group_lanes > 4) join(of_lane_xor<4>(a), of_lane_xor<4>(b));
+    if (p.group_lanes > 8) join(of_lane_xor<8>(a), of_lane_xor<8>(b));
+    if (p.group_lanes > 16) join(of_lane_xor<16>(a), of_lane_xor<16>(b));
     const V rating = p.best == 2 && b > none ? a + b : a;
     const int from = base + ((at * p.group_lanes) & (LPT - 1));
     V r;
