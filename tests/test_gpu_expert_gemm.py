@@ -103,7 +103,7 @@ def test_product_many_experts(rows, E):
 
 
 # (experts, rows, n, k): every kernel of the product (16 rows by 16 and 64 columns, 32 rows by 64 and 128, 128 and
-# 256 rows a block) and of the SwiGLU form (16, 32 and 128 rows a block); the last ones give every wave that shares
+# 256 rows a block) and of the SwiGLU form (16, 32, 64 and 128 rows a block); the last ones give every wave that shares
 # the channels several blocks of them
 KERNELS = [(1, 3, 256, 640), (3, 90, 256, 640), (40, 130, 1024, 384), (70, 100, 2048, 128), (6, 700, 2048, 256),
            (3, 900, 1024, 128), (2, 1300, 8192, 128), (1, 4400, 2048, 128), (40, 700, 2048, 384),
