@@ -280,11 +280,16 @@ __global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(Gemm
             if (busy) multiply(now);
             end_step<kLoads>();
         };
-        for (int b = 0; b < blocks; b += 3) {
+        // (three steps a turn and no way round any of them: else the compiler would find loads under way
+        // that no path has there, and wait for them)
+        int b = 0;
+        for (; b + 3 <= blocks; b += 3) {
             step(s_0, s_2, b);
-            if (b + 1 < blocks) step(s_1, s_0, b + 1);
-            if (b + 2 < blocks) step(s_2, s_1, b + 2);
+            step(s_1, s_0, b + 1);
+            step(s_2, s_1, b + 2);
         }
+        if (b < blocks) step(s_0, s_2, b);
+        if (b + 1 < blocks) step(s_1, s_0, b + 1);
     } else {
         static_assert(MI % 2 == 0, "rows alternate between two sets of registers");
         i32x8 cw[2][2], cx[2][2];  // codes of the weights; of the rows in hand and of the next
@@ -344,12 +349,15 @@ __global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(Gemm
             read(s_0 + kW + wn * 64 * kUnits, cw[0]);
             read(s_0 + kW + (wn * 64 + 32) * kUnits, cw[1]);
         }
-        for (int b = 0; b < blocks; b += STAGES) {
+        int b = 0;
+        for (; b + STAGES <= blocks; b += STAGES) {  // no way round a step: as above
             step(s_0, s_1, b);
-            if (b + 1 < blocks) step(s_1, STAGES == 3 ? s_2 : s_0, b + 1);
-            if constexpr (STAGES == 3)
-                if (b + 2 < blocks) step(s_2, s_0, b + 2);
+            step(s_1, STAGES == 3 ? s_2 : s_0, b + 1);
+            if constexpr (STAGES == 3) step(s_2, s_0, b + 2);
         }
+        if (b < blocks) step(s_0, s_1, b);
+        if constexpr (STAGES == 3)
+            if (b + 1 < blocks) step(s_1, s_2, b + 1);
         add(acc[MI - 1][1], part[1], keep);
     }
 
