@@ -668,13 +668,13 @@ Plan narrow() {
 //   mean rows               4    8   12   16   24   32   48   64   96  128  192  256  512
 //   SwiGLU   s 1, 4, 4, 2 165  165  194  192  237  262
 //            s 2, 4, 4, 2 170  168  170  172  217  229
-//            wide 64           162  162  163  166  169  173  233  303  399  525  677 1241
-//            wide 128          187  170  170       172       219  263  405  484  600 1060
+//            wide 64      163  163  163  164  165  168  175  237  297  388  532  664 1181
+//            wide 128     168  168  168  169  169  173  173  219  248  388  477  601 1051
 //   product  s 1, 4, 1, 8  80   83   88   98  120  134
 //            s 2, 4, 1, 8 105  111  110  113  122  145
 //            s 2, 4, 2, 2  86   91   92   92   96  111  128
-//            wide 128          104  103  103       105       106  113  146  178  219  387
-//            wide 256                                        122  125  137  155  195  335
+//            wide 128     101  101  103  104  105  104  104  105  107  138  169  210  364
+//            wide 256     118  121  120  119  120  119  120  121  125  137  151  198  334
 // Where there are fewer blocks than compute units a block's own time counts, and more waves of a block
 // on the channels, or fewer columns a block, shorten it.  One expert, product of 7168 channels to 2048
 // and of 2048 to 7168, and SwiGLU of 7168 to 2048, us:
@@ -682,12 +682,12 @@ Plan narrow() {
 //   product  s 1, 1, 1, 8   6    8   13   24   44                     |   6   20   36
 //            s 1, 4, 1, 8   9   11   11   13   20   34   65           |   6    9   15   24
 //            s 2, 4, 1, 8  11   13   15   15   16   28   54  105      |   7    8   13   25   79
-//            wide 128           36   39   59   59   59   59   63   84 |       15   20   21   23   44   94
-//            wide 256                            96   96   96   96  101 |                 31   32   38   77
+//            wide 128      34   35   36   55   55   56   57   61   75 |  13   14   20   20   23   44   92
+//            wide 256      57   57   59   63   95   95   95   98  101 |  21   21   22   31   33   38   76
 //   SwiGLU   s 1, 4, 4, 2  36   37   37   37   40   79  151
 //            s 2, 4, 4, 2  43   44   47   46   47   52  101  199
-//            wide 64       38   39   59   59   60   61   72  142  287
-//            wide 128      57   58   58   91   91   92   96  128  237
+//            wide 64       38   39   59   60   61   64   81  151  285
+//            wide 128      57   57   57   90   91   93   96  133  236
 constexpr int kComputeUnits = 256;
 Plan plan(const GemmArgs &a) {
     const int64_t mean = a.num_rows / a.num_experts;
