@@ -568,7 +568,8 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_kernel(RouteParams p
     const int chosen = at < p.K ? s_chosen[slot][at].expert : -1;
     double s = 0.0;
     if (chosen >= 0) {
-        const double l = load_logit<BF16>(p.a.logits, row + chosen);
+        // with no bias the logit is what it was chosen by
+        const double l = p.a.bias == nullptr ? value_of(s_chosen[slot][at].key) : load_logit<BF16>(p.a.logits, row + chosen);
         s = p.sigmoid ? 1.0 / (1.0 + exp(-l)) : l;
     }
     if (!p.sigmoid) {

@@ -62,15 +62,20 @@ _MASK = (torch.uint8, torch.bool)
 _LOGITS = {torch.float32: EP_LOGITS_F32, torch.bfloat16: EP_LOGITS_BF16}
 
 
+# what every call asks for: small calls cost the host more than they cost the GPU
+_initialized, _current_device, _current_stream = (torch.cuda.is_initialized, torch._C._cuda_getDevice,
+                                                  torch._C._cuda_getCurrentRawStream)
+
+
 def _device() -> int:
     """The current GPU; none before the first use of one, when no tensor can be on it."""
-    return torch._C._cuda_getDevice() if torch.cuda.is_initialized() else -2
+    return _current_device() if _initialized() else -2
 
 
 def _raw_stream(stream, device) -> int | None:
     # the handle alone: building torch's stream object costs as much as the rest of a small call
     if stream is None and device >= 0:
-        return torch._C._cuda_getCurrentRawStream(device)
+        return _current_stream(device)
     if isinstance(stream, torch.cuda.Stream) and stream.device_index != device:
         raise ValueError(f"stream: on GPU {stream.device_index}, not on the current one")
     return _stream(stream)
@@ -98,6 +103,9 @@ def _logit_rows(name, t, tokens, experts, device, dtype=None) -> int:
     """The stride between rows of a [tokens][experts] tensor whose rows may lie apart."""
     if t is None:
         _refuse(name, t, f"[{tokens}][{experts}] of {dtype or 'float32 or bfloat16'}")
+    if t.shape == (tokens, experts) and t.is_contiguous() and t.get_device() == device and t.dtype in _LOGITS and \
+            (dtype is None or t.dtype == dtype):
+        return experts
     rows, columns = t.shape if t.dim() == 2 else (-1, -1)
     apart, along = t.stride() if t.dim() == 2 else (0, 0)
     if t.get_device() != device or t.dtype not in _LOGITS or (dtype is not None and t.dtype != dtype) or \
