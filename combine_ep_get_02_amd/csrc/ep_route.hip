@@ -27,7 +27,7 @@ struct RouteParams {
     int64_t T;
     int E, K, G, kept, best, group_size;
     int group_lanes;  // lanes of a token that share a group: a power of two, of all lanes over G
-    bool sigmoid, renorm, vector;
+    bool sigmoid, renorm;
     float scale;
 };
 
@@ -35,7 +35,7 @@ struct RouteBackwardParams {
     RouteBackwardArgs a;
     int64_t T;
     int E, K;
-    bool sigmoid, renorm, vector, vector_out;
+    bool sigmoid, renorm;
     float scale;
 };
 
@@ -51,39 +51,67 @@ __device__ __forceinline__ double shfl_f64(double v, int from) {
     return __builtin_bit_cast(double, ((uint64_t)hi << 32) | lo);
 }
 
-// VPL logits that start on a boundary of their own size (or of 16 bytes where they are more).
-template <int VPL, bool BF16>
-__device__ __forceinline__ void load_logits(const void *p, int64_t i, float (&out)[VPL]) {
-    if constexpr (BF16) {
-        const uint16_t *src = static_cast<const uint16_t *>(p) + i;
-        constexpr int W = VPL < 8 ? VPL : 8;
-        typedef uint16_t vec __attribute__((ext_vector_type(W)));
+// VPL values of a row from element i on, `left` of them there (the others are left as they are).  Where
+// all are, in words of up to 16 bytes, which need not lie on boundaries of more than 4.
+template <int VPL>
+__device__ __forceinline__ void load_values(const float *p, int64_t i, int left, float (&out)[VPL]) {
+    constexpr int W = VPL < 4 ? VPL : 4;
+    typedef float vec __attribute__((ext_vector_type(W), aligned(4)));
+    if (left >= VPL) {
 #pragma unroll
         for (int k = 0; k < VPL; k += W) {
-            const vec v = *reinterpret_cast<const vec *>(src + k);
-#pragma unroll
-            for (int u = 0; u < W; ++u) out[k + u] = __uint_as_float((uint32_t)v[u] << 16);
-        }
-    } else {
-        const float *src = static_cast<const float *>(p) + i;
-        constexpr int W = VPL < 4 ? VPL : 4;
-        typedef float vec __attribute__((ext_vector_type(W)));
-#pragma unroll
-        for (int k = 0; k < VPL; k += W) {
-            const vec v = *reinterpret_cast<const vec *>(src + k);
+            const vec v = *reinterpret_cast<const vec *>(p + i + k);
 #pragma unroll
             for (int u = 0; u < W; ++u) out[k + u] = v[u];
+        }
+    } else {
+#pragma unroll
+        for (int k = 0; k < VPL; ++k)
+            if (k < left) out[k] = p[i + k];
+    }
+}
+
+__device__ __forceinline__ bool on_words(const void *p) { return (reinterpret_cast<uintptr_t>(p) & 3) == 0; }
+
+template <int VPL, bool BF16>
+__device__ __forceinline__ void load_logits(const void *p, int64_t i, int left, float (&out)[VPL]) {
+    if constexpr (!BF16) {
+        load_values<VPL>(static_cast<const float *>(p), i, left, out);
+    } else {
+        constexpr int W = VPL < 2 ? 1 : VPL < 8 ? VPL / 2 : 4;
+        typedef uint32_t vec __attribute__((ext_vector_type(W), aligned(4)));
+        const uint16_t *src = static_cast<const uint16_t *>(p) + i;
+        if (VPL > 1 && left >= VPL && on_words(src)) {
+#pragma unroll
+            for (int k = 0; k < VPL; k += 2 * W) {
+                const vec v = *reinterpret_cast<const vec *>(src + k);
+#pragma unroll
+                for (int u = 0; u < 2 * W && k + u < VPL; ++u) out[k + u] = u % 2 == 0 ? bf16_low(v[u / 2]) : bf16_high(v[u / 2]);
+            }
+        } else {
+#pragma unroll
+            for (int k = 0; k < VPL; ++k)
+                if (k < left) out[k] = __uint_as_float((uint32_t)src[k] << 16);
         }
     }
 }
 
 template <int VPL, bool BF16>
-__device__ __forceinline__ void store_logits(void *p, int64_t i, const float (&v)[VPL]) {
-    if constexpr (BF16 && VPL == 1) {
+__device__ __forceinline__ void store_logits(void *p, int64_t i, int left, const float (&v)[VPL]) {
+    if (left < VPL || (BF16 && !on_words(static_cast<uint16_t *>(p) + i))) {
+#pragma unroll
+        for (int k = 0; k < VPL; ++k) {
+            if (k >= left) continue;
+            if constexpr (BF16)
+                static_cast<uint16_t *>(p)[i + k] = (uint16_t)pack_bf16(v[k], 0.0f);
+            else
+                static_cast<float *>(p)[i + k] = v[k];
+        }
+    } else if constexpr (BF16 && VPL == 1) {
         static_cast<uint16_t *>(p)[i] = (uint16_t)pack_bf16(v[0], 0.0f);
     } else if constexpr (BF16) {
         constexpr int W = VPL < 8 ? VPL / 2 : 4;
-        typedef uint32_t vec __attribute__((ext_vector_type(W)));
+        typedef uint32_t vec __attribute__((ext_vector_type(W), aligned(4)));
 #pragma unroll
         for (int k = 0; k < VPL; k += 2 * W) {
             vec w;
@@ -93,7 +121,7 @@ __device__ __forceinline__ void store_logits(void *p, int64_t i, const float (&v
         }
     } else {
         constexpr int W = VPL < 4 ? VPL : 4;
-        typedef float vec __attribute__((ext_vector_type(W)));
+        typedef float vec __attribute__((ext_vector_type(W), aligned(4)));
 #pragma unroll
         for (int k = 0; k < VPL; k += W) {
             vec w;
@@ -530,22 +558,13 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_kernel(RouteParams p
     Part<VPL> part;
     part.first = at * VPL;
     bool bad = false;
-    if (p.vector) {  // a lane's logits are whole aligned words, and all of them in or out
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) part.logit[i] = -INFINITY;
-        if (on && part.first < p.E) load_logits<VPL, BF16>(p.a.logits, row + part.first, part.logit);
-    } else {
-#pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            part.logit[i] = -INFINITY;
-            if (on && part.first + i < p.E) part.logit[i] = load_logit<BF16>(p.a.logits, row + part.first + i);
-        }
-    }
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
+        part.logit[i] = -INFINITY;
         part.bias[i] = 0.0f;
-        if (p.a.bias != nullptr && part.first + i < p.E) part.bias[i] = p.a.bias[part.first + i];
     }
+    if (on) load_logits<VPL, BF16>(p.a.logits, row + part.first, p.E - part.first, part.logit);
+    if (p.a.bias != nullptr) load_values<VPL>(p.a.bias, part.first, p.E - part.first, part.bias);
 #pragma unroll
     for (int i = 0; i < VPL; ++i) {
         if (unusable(part.logit[i])) {
@@ -630,13 +649,7 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_backward_kernel(Rout
 #pragma unroll
         for (int i = 0; i < VPL; ++i) logit[i] = -INFINITY;
         const int e = from + at * VPL;
-        if (p.vector) {  // a lane's logits are whole aligned words, and all of them in or out
-            if (on && e < p.E) load_logits<VPL, BF16>(p.a.logits, row + e, logit);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                if (on && e + i < p.E) logit[i] = load_logit<BF16>(p.a.logits, row + e + i);
-        }
+        if (on) load_logits<VPL, BF16>(p.a.logits, row + e, p.E - e, logit);
 #pragma unroll
         for (int i = 0; i < VPL; ++i) {
             if (unusable(logit[i])) {
@@ -709,33 +722,14 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_backward_kernel(Rout
         }
         if (!here) continue;
         const int64_t out = t * p.a.grad_stride + e0;
-        if (p.vector_out) {
-            if (e0 < p.E) store_logits<VPL, BF16>(p.a.grad_logits, out, d);
-        } else {
-#pragma unroll
-            for (int i = 0; i < VPL; ++i) {
-                if (e0 + i >= p.E) continue;
-                if constexpr (BF16)
-                    static_cast<uint16_t *>(p.a.grad_logits)[out + i] = (uint16_t)pack_bf16(d[i], 0.0f);
-                else
-                    static_cast<float *>(p.a.grad_logits)[out + i] = d[i];
-            }
-        }
+        store_logits<VPL, BF16>(p.a.grad_logits, out, p.E - e0, d);
     }
     if (ballot64(bad) != 0ull && lane == 0) flag(p.a.dev_status, EP_DEV_BAD_LOGIT);
-}
-
-// Whether rows of E values `stride` apart from p let a lane move VPL of them as whole words.
-template <int VPL, bool BF16>
-bool whole_words(const void *p, int64_t stride, int E) {
-    const int64_t size = BF16 ? 2 : 4, word = VPL * size, unit = word < 16 ? word : 16;
-    return E % VPL == 0 && reinterpret_cast<uintptr_t>(p) % unit == 0 && stride * size % unit == 0;
 }
 
 template <int LPT, int VPL, bool BF16>
 hipError_t start(RouteParams p, hipStream_t stream) {
     constexpr int kTokens = kRouteWaves * kWave / LPT;
-    p.vector = whole_words<VPL, BF16>(p.a.logits, p.a.stride, p.E);
     p.group_lanes = 1;
     while (2 * p.group_lanes * p.G <= LPT) p.group_lanes *= 2;
     hipLaunchKernelGGL((route_kernel<LPT, VPL, BF16>), dim3((unsigned)((p.T + kTokens - 1) / kTokens)),
@@ -745,8 +739,6 @@ hipError_t start(RouteParams p, hipStream_t stream) {
 template <int LPT, int VPL, bool BF16>
 hipError_t start(RouteBackwardParams p, hipStream_t stream) {
     constexpr int kTokens = kRouteWaves * kWave / LPT;
-    p.vector = whole_words<VPL, BF16>(p.a.logits, p.a.stride, p.E);
-    p.vector_out = whole_words<VPL, BF16>(p.a.grad_logits, p.a.grad_stride, p.E);
     hipLaunchKernelGGL((route_backward_kernel<LPT, VPL, BF16>), dim3((unsigned)((p.T + kTokens - 1) / kTokens)),
                        dim3(kRouteWaves * kWave), 0, stream, p);
     return hipGetLastError();
