@@ -275,6 +275,33 @@ def test_rows_apart(dtype):
         _check_gradient(out[:, lead:lead + E], values, got_i, gw, "sigmoid", True, 1.0)
 
 
+@pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
+@pytest.mark.parametrize("T,E", [(50, 100), (50, 200), (30, 471), (2100, 61), (2100, 120), (2100, 255), (9, 1501)])
+def test_rows_apart_equal_rows_together(T, E, dtype):
+    """Rows that start on any element, of whole and of part lanes: the same bits as rows without gaps."""
+    rng = np.random.default_rng(T + E)
+    k = 5
+    _, logits = _logits(rng, T, E, dtype)
+    bias = torch.from_numpy((rng.standard_normal(E) * 0.1).astype(np.float32)).cuda()
+    gw = torch.from_numpy(rng.standard_normal((T, k)).astype(np.float32)).cuda()
+    shape, r = ep.make_shape(T, 8, k, E, 1, 1), experts.make_router(experts.EP_SCORE_SOFTMAX)
+    want_i, want_w, status = _route(logits, bias, "softmax", k)
+    idx = torch.from_numpy(want_i).cuda()
+    grad = torch.empty_like(logits)
+    experts.ep_route_backward(shape, r, logits, idx, gw, grad)
+    for lead, extra in ((1, 0), (2, 1), (3, 6), (0, 1)):
+        wide = torch.full((T, lead + E + extra), float("nan"), dtype=dtype, device="cuda")
+        wide[:, lead:lead + E] = logits
+        shifted = torch.full((E + lead,), float("nan"), device="cuda")
+        shifted[lead:] = bias
+        got_i, got_w, status = _route(wide[:, lead:lead + E], shifted[lead:], "softmax", k)
+        assert np.array_equal(got_i, want_i) and np.array_equal(got_w, want_w) and status == 0
+        out = torch.full_like(wide, 7.0)
+        experts.ep_route_backward(shape, r, wide[:, lead:lead + E], idx, gw, out[:, lead:lead + E])
+        assert torch.equal(out[:, lead:lead + E], grad)
+        assert bool((out[:, :lead] == 7.0).all()) and bool((out[:, lead + E:] == 7.0).all())
+
+
 def _check_gradient(got, values, idx, gw, kind, renorm, scale):
     want, size, before = oracle64.route_backward(values, idx, gw, kind, renorm, scale)
     # sigmoid: two 32-bit sigmoids of at most 8 U each (an exponential, a sum, a quotient), the slots'
