@@ -211,8 +211,7 @@ hipError_t launch_combine_grouped(const ep_shape_t &s, const CombineGroupedArgs 
     Params p = params(s, a);
     p.segments = (p.units + kWave - 1) / kWave;
     const int64_t blocks = (p.T * p.segments + kWaves - 1) / kWaves;
-    hipLaunchKernelGGL(combine_grouped_kernel, dim3((unsigned)blocks), dim3(kWaves * kWave), 0, stream, p);
-    return hipGetLastError();
+    return start_kernel(combine_grouped_kernel, blocks, kWaves * kWave, stream, p);
 }
 
 hipError_t launch_combine_grouped_backward(const ep_shape_t &s, const CombineGroupedArgs &a, hipStream_t stream) {
@@ -221,16 +220,10 @@ hipError_t launch_combine_grouped_backward(const ep_shape_t &s, const CombineGro
     int64_t blocks = a.num_rows / 16 < 1024 ? a.num_rows / 16 + 1 : 1024;
     if (p.T > blocks) blocks = p.T;
     if (p.T == 0 && a.num_rows == 0) return hipSuccess;
-    auto start = [&](auto kernel, int waves) {
-        hipLaunchKernelGGL(kernel, dim3((unsigned)blocks), dim3(waves * kWave), 0, stream, p);
-    };
     // rows up to 4 KiB in one turn of four waves; wider ones take 8 waves of two units (16 KiB a turn):
     // 4096-wide rows 292-300 us at 16384 tokens (5.3 TB/s), as 4 or 16 waves do
-    if (p.units <= 4 * kWave)
-        start(combine_grouped_backward_kernel<4, 1>, 4);
-    else
-        start(combine_grouped_backward_kernel<8, 2>, 8);
-    return hipGetLastError();
+    if (p.units <= 4 * kWave) return start_kernel(combine_grouped_backward_kernel<4, 1>, blocks, 4 * kWave, stream, p);
+    return start_kernel(combine_grouped_backward_kernel<8, 2>, blocks, 8 * kWave, stream, p);
 }
 
 }  // namespace ep

@@ -734,8 +734,7 @@ hipError_t launch_expert_gemm(const GemmArgs &a, hipStream_t stream) {
     const Plan pl = plan(a);
     const int64_t blocks = grid_blocks(a, pl);
     if (blocks == 0) return hipSuccess;
-    hipLaunchKernelGGL(pl.kernel, dim3((unsigned)blocks), dim3(pl.threads), 0, stream, a, (a.n + pl.cols - 1) / pl.cols);
-    return hipGetLastError();
+    return start_kernel(pl.kernel, blocks, pl.threads, stream, a, (a.n + pl.cols - 1) / pl.cols);
 }
 
 }  // namespace ep

@@ -76,6 +76,16 @@ struct CombineGroupedArgs {
 hipError_t launch_combine_grouped(const ep_shape_t &s, const CombineGroupedArgs &a, hipStream_t stream);
 hipError_t launch_combine_grouped_backward(const ep_shape_t &s, const CombineGroupedArgs &a, hipStream_t stream);
 
+// A launch without the triple brackets' pushed and popped configuration: 0.2 us less of the host's 3.7.
+template <typename... A>
+hipError_t start_kernel(void (*kernel)(A...), int64_t blocks, int threads, hipStream_t stream, A... a) {
+    void *args[] = {&a...};
+    const hipError_t e = hipLaunchKernel(reinterpret_cast<const void *>(kernel), dim3((unsigned)blocks), dim3(threads),
+                                         args, 0, stream);
+    if (e != hipSuccess) (void)hipGetLastError();  // it is reported here, and not again by a later call
+    return e;
+}
+
 // Two f32 to a pair of bf16 in one word, nearest, ties to even, NaN kept (v_cvt_pk_bf16_f32).
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));

@@ -732,16 +732,12 @@ hipError_t start(RouteParams p, hipStream_t stream) {
     constexpr int kTokens = kRouteWaves * kWave / LPT;
     p.group_lanes = 1;
     while (2 * p.group_lanes * p.G <= LPT) p.group_lanes *= 2;
-    hipLaunchKernelGGL((route_kernel<LPT, VPL, BF16>), dim3((unsigned)((p.T + kTokens - 1) / kTokens)),
-                       dim3(kRouteWaves * kWave), 0, stream, p);
-    return hipGetLastError();
+    return start_kernel(route_kernel<LPT, VPL, BF16>, (p.T + kTokens - 1) / kTokens, kRouteWaves * kWave, stream, p);
 }
 template <int LPT, int VPL, bool BF16>
 hipError_t start(RouteBackwardParams p, hipStream_t stream) {
     constexpr int kTokens = kRouteWaves * kWave / LPT;
-    hipLaunchKernelGGL((route_backward_kernel<LPT, VPL, BF16>), dim3((unsigned)((p.T + kTokens - 1) / kTokens)),
-                       dim3(kRouteWaves * kWave), 0, stream, p);
-    return hipGetLastError();
+    return start_kernel(route_backward_kernel<LPT, VPL, BF16>, (p.T + kTokens - 1) / kTokens, kRouteWaves * kWave, stream, p);
 }
 
 template <bool BF16>
