@@ -143,12 +143,12 @@ __device__ __forceinline__ bool unusable(float v) { return !(v < INFINITY); }
 
 // How far apart two f32 choices have to be for their order to be sure: kSlack of the larger one's size
 // and kSigmoidSlack, or kSoftmaxSlack of the token's largest score.  With u = 2^-24: an exponential is off by
-// (|argument| + 2) u of it at most, which for the argument l - max of a softmax is under 2 u of 1, and
-// for a sigmoid (whose argument is exact) under 2 u of the score; sum and quotient of a sigmoid add
-// 2 u, the bias u of the choice.  A softmax divides by a sum whose terms are off by the same and whose
-// 38 additions at most by u each: under 60 u of the largest score.  Twice that for two sides, and half
-// as much again to spare.
-constexpr float kSlack = 16 * 0x1p-24f, kSigmoidSlack = 16 * 0x1p-24f, kSoftmaxSlack = 180 * 0x1p-24f;
+// (|argument| + 2) u of it at most.  A sigmoid's argument -l is exact, and its exponential weighs (1 - s) in
+// the score: s (1 - s) (|l| + 2) u < 0.6 u.  Its sum and its quotient add s u each, so it is off by under
+// 2.6 u; adding the bias by u of the choice.  The argument l - max of a softmax leaves its exponential under
+// 2 u of 1 off; it divides by a sum whose terms are off by the same and whose 38 additions at most by u each:
+// under 60 u of the largest score.  Twice that for two sides, and half as much again to spare.
+constexpr float kSlack = 4 * 0x1p-24f, kSigmoidSlack = 8 * 0x1p-24f, kSoftmaxSlack = 180 * 0x1p-24f;
 
 // f32 to an integer that orders as it does (+0 and -0 alike); kNone is below all of them.
 constexpr int kNone = INT_MIN;
@@ -239,7 +239,7 @@ struct Part {
 
 // Which groups stay, as a bit each (a rating orders as `exact` or `rough` does, ties to the lower
 // group), from lane g's rating of group g.  Returns in *close whether a group kept and one dropped
-// are no further apart than `slack` and twice kSlack of the rating's size.
+// are no further apart than one of their `slack`s.
 template <int LPT, typename F>
 __device__ __forceinline__ uint64_t keep_groups(F rating, int G, int kept, float slack, int lane, bool *close) {
     const int at = lane & (LPT - 1), base = lane & (kWave - LPT);
@@ -260,10 +260,11 @@ __device__ __forceinline__ uint64_t keep_groups(F rating, int G, int kept, float
     if (close != nullptr) {
         bool near = false;
         for (int g = 0; g < G; ++g) {
-            const float o = (float)rating_of(g), r = (float)rating;
-            // -inf (a group without experts to choose) is near nothing
-            near |= at < G && ((bits >> g) & 1ull) != (uint64_t)stays && fabsf(o - r) <= slack + 2.0f * kSlack * fabsf(r);
+            const bool other = ((bits >> g) & 1ull) != (uint64_t)stays;
+            near |= other && !(fabsf((float)rating_of(g) - (float)rating) > slack);
         }
+        // -inf (a group without experts to choose) is near nothing; a sum that overflows is near all
+        near &= at < G && rating > -INFINITY;
         *close = token_bits<LPT>(ballot64(near), lane) != 0ull;
     }
     return bits;
@@ -310,9 +311,10 @@ __device__ __forceinline__ void exact_choices(const RouteParams &p, const Part<V
 }
 
 // Lane g: the rating of group g (-inf without experts), from the token's choices in LDS (those of the
-// wave's lane l from choice[l], kWave apart).  group_lanes lanes share a group's experts.
+// wave's lane l from choice[l], kWave apart).  group_lanes lanes share a group's experts.  *size: the
+// sum of what the rating adds up, without signs.
 template <int LPT, int VPL, typename V>
-__device__ __forceinline__ V rate_groups(const RouteParams &p, const V *choice, int lane) {
+__device__ __forceinline__ V rate_groups(const RouteParams &p, const V *choice, int lane, float *size) {
     const int at = lane & (LPT - 1), base = lane & (kWave - LPT);
     const V none = -INFINITY;
     const int g = at / p.group_lanes;
@@ -338,11 +340,16 @@ __device__ __forceinline__ V rate_groups(const RouteParams &p, const V *choice, 
     if (p.group_lanes > 4) join(of_lane_xor<4>(a), of_lane_xor<4>(b));
     if (p.group_lanes > 8) join(of_lane_xor<8>(a), of_lane_xor<8>(b));
     if (p.group_lanes > 16) join(of_lane_xor<16>(a), of_lane_xor<16>(b));
-    const V rating = p.best == 2 && b > none ? a + b : a;
+    const bool two = p.best == 2 && b > none;
+    const V rating = two ? a + b : a;
     const int from = base + ((at * p.group_lanes) & (LPT - 1));
     V r;
-    if constexpr (sizeof(V) == 8) r = shfl_f64(rating, from);
-    else r = __shfl(rating, from);
+    if constexpr (sizeof(V) == 8) {
+        r = shfl_f64(rating, from);
+    } else {
+        r = __shfl(rating, from);
+        *size = __shfl(two ? fabsf(a) + fabsf(b) : fabsf(a), from);
+    }
     return at < p.G ? r : none;
 }
 
@@ -426,15 +433,17 @@ __device__ __forceinline__ void choose(const RouteParams &p, const Part<VPL> &t,
         for (int i = 0; i < VPL; ++i)
             rough[i * kWave + lane] = key[i] == kNone ? -INFINITY : by_logit ? t.logit[i] : choice[i];
         wave_lds_order();
-        const float rating = rate_groups<LPT, VPL>(p, rough, lane);
+        float size;
+        const float rating = rate_groups<LPT, VPL>(p, rough, lane, &size);
         wave_lds_order();
         bool close = false;
-        keep = keep_groups<LPT>(rating, p.G, p.kept, 2.0f * slack, lane, by_logit ? nullptr : &close);
+        // two choices and their sum's rounding on either side
+        keep = keep_groups<LPT>(rating, p.G, p.kept, 2.0f * (slack + kSlack * size), lane, by_logit ? nullptr : &close);
         if (ballot64(close) != 0ull) {
             exact_choices<LPT, VPL>(p, t, &exact[0][lane]);
             have_exact = true;
             wave_lds_order();
-            const double sure = rate_groups<LPT, VPL>(p, &exact[0][0], lane);
+            const double sure = rate_groups<LPT, VPL>(p, &exact[0][0], lane, nullptr);
             keep = keep_groups<LPT>(sure, p.G, p.kept, 0.0f, lane, nullptr);
         }
     }

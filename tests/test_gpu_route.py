@@ -176,6 +176,21 @@ def test_groups(E, groups, kept, best, kind, with_bias):
     _weights_near(got_w, want_w, kind, True)
 
 
+@pytest.mark.parametrize("T", [300, 2100])
+@pytest.mark.parametrize("kind", sorted(KINDS))
+def test_group_ratings_that_cancel(T, kind):
+    """The two best of each group are about 64 and -64: their sum is far smaller than what f32 makes of each is off by."""
+    rng = np.random.default_rng(T)
+    E, groups = 16, 8
+    values = np.repeat(rng.standard_normal((T, 1)), E, 1).astype(np.float32)
+    values += (rng.integers(-8, 9, size=(T, E)) * 2.0 ** -21).astype(np.float32)
+    bias = np.tile(np.array([64, -64], np.float32), groups)
+    got_i, got_w, _ = _route(torch.from_numpy(values).cuda(), torch.from_numpy(bias).cuda(), kind, 3, groups, 3, 2)
+    want_i, want_w = oracle64.route(values, bias, kind, 3, groups, 3, 2, True, 1.0)
+    assert np.array_equal(got_i, want_i)
+    _weights_near(got_w, want_w, kind, True)
+
+
 @pytest.mark.parametrize("kind", sorted(KINDS))
 @pytest.mark.parametrize("with_bias", [False, True])
 def test_ties_go_to_the_lowest_expert(kind, with_bias):
