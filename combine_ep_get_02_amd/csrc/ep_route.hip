@@ -260,8 +260,8 @@ __device__ __forceinline__ uint64_t keep_groups(F rating, int G, int kept, float
     if (close != nullptr) {
         bool near = false;
         for (int g = 0; g < G; ++g) {
-            const bool other = ((bits >> g) & 1ull) != (uint64_t)stays;
-            near |= other && !(fabsf((float)rating_of(g) - (float)rating) > slack);
+            const float o = (float)rating_of(g);  // by all lanes, whether they need it or not
+            near |= ((bits >> g) & 1ull) != (uint64_t)stays && !(fabsf(o - (float)rating) > slack);
         }
         // -inf (a group without experts to choose) is near nothing; a sum that overflows is near all
         near &= at < G && rating > -INFINITY;
