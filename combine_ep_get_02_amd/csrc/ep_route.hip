@@ -1,8 +1,8 @@
 // ep_route.hip -- the router: a token's scores, the experts chosen from them and their weights, and
 // the gradient of the weights (gfx950).  Definitions in ep_experts.h.
 //
-// A token is 64 lanes or, where there are many tokens and few experts, 16 (four tokens a wave: a
-// round of the selection then costs its cross-lane steps once for four).  Lane i of a token holds
+// A token is 64 lanes or, where there are many tokens and few experts, 32 or 16 (a round of the selection
+// then costs its cross-lane steps once for two or four tokens of a wave).  Lane i of a token holds
 // the VPL consecutive experts from i * VPL, so the lowest lane with the largest value, then the
 // lowest element in it, is the lowest expert: ties need no index.
 //
@@ -20,7 +20,15 @@ namespace ep {
 namespace {
 
 constexpr int kRouteWaves = 4;  // waves per block
-constexpr int64_t kManyTokens = 2048;
+// From this many tokens on they share waves.  Few tokens are bound by the latency of one wave's steps, which
+// more experts a lane lengthen; many by the vector instructions of all.  8 slots, router (softmax) / its
+// gradient with 64, 32 and 16 lanes, us:
+//   tokens                    2048                          4096                          16384
+//   64 experts                4.6/4.2  4.6/4.3  4.8/4.6     5.5/5.4  4.9/4.6  4.8/4.7     13.0/13.4  9.2/8.7  6.5/6.9
+//   128 experts               4.8/4.6  4.9/4.8  5.5/5.5     6.0/6.2  5.4/5.3  5.6/5.8     14.5/14.7  10.4/11.1  8.0/9.2
+//   256 experts in 8 groups   7.9/5.3  9.1/6.0  17.7/-      11/7.3   10/6.8   18/-        29/18.6    25/15.3    30/-
+// (512 experts in 8 groups, 16384 tokens, 64 and 32 lanes: 40/30 and 41/30.)
+constexpr int64_t kManyTokens = 4096;
 
 struct RouteParams {
     RouteArgs a;
@@ -173,7 +181,7 @@ __device__ __forceinline__ int token_max(int v) {
 #undef EP_MAX_STEP
         return readlane32(v, kWave - 1);
     } else {
-        static_assert(LPT == 16, "a row of 16 lanes");
+        static_assert(LPT == 16 || LPT == 32, "one row of 16 lanes or two");
         int o = (int)lane_xor<1>((uint32_t)v);
         v = o > v ? o : v;
         o = (int)lane_xor<2>((uint32_t)v);
@@ -181,7 +189,12 @@ __device__ __forceinline__ int token_max(int v) {
         o = (int)lane_xor<4>((uint32_t)v);
         v = o > v ? o : v;
         o = (int)lane_xor<8>((uint32_t)v);
-        return o > v ? o : v;
+        v = o > v ? o : v;
+        if constexpr (LPT == 32) {
+            o = (int)lane_xor<16>((uint32_t)v);
+            v = o > v ? o : v;
+        }
+        return v;
     }
 }
 
@@ -207,6 +220,7 @@ __device__ __forceinline__ F token_sum(F v) {
     v += of_lane_xor<2>(v);
     v += of_lane_xor<4>(v);
     v += of_lane_xor<8>(v);
+    if constexpr (LPT == 32) v += of_lane_xor<16>(v);
     if constexpr (LPT == kWave) v = (of_lane(v, 0) + of_lane(v, 16)) + (of_lane(v, 32) + of_lane(v, 48));
     return v;
 }
@@ -552,6 +566,9 @@ __device__ __forceinline__ void choose(const RouteParams &p, const Part<VPL> &t,
         if (place[u] < p.K) chosen[place[u]].expert = expert[u];
 }
 
+// One launch routes a token per LPT lanes.  128 tokens of 256 experts in 8 groups take 7.3 us on the card, a
+// launch (about 3) included: latency, of loads, group ratings and a chain of cross-lane steps a slot.  16384
+// tokens of 64 experts take 6 us, over the 0.6 that their bytes need, for the same reason.
 template <int LPT, int VPL, bool BF16>
 __global__ __launch_bounds__(kRouteWaves *kWave) void route_kernel(RouteParams p) {
     constexpr int kTokens = kWave / LPT;  // of a wave
@@ -633,7 +650,9 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_kernel(RouteParams p
     }
 }
 
-// VPL experts a lane at a time, all of a token's at once where they fit.
+// VPL experts a lane at a time, all of a token's at once where they fit.  4096 tokens of 256 experts take 6.8 us on
+// the card (8.8 MB, 1.7 us of bytes), 16384 tokens of 64 in bf16 6.3 us: a launch and the latency of one wave's
+// loads, sums over its slots and stores.
 template <int LPT, int VPL, bool BF16>
 __global__ __launch_bounds__(kRouteWaves *kWave) void route_backward_kernel(RouteBackwardParams p) {
     constexpr int kTokens = kWave / LPT, kSpan = LPT * VPL;
@@ -751,10 +770,12 @@ hipError_t start(RouteBackwardParams p, hipStream_t stream) {
 
 template <bool BF16>
 hipError_t start_route(const RouteParams &p, hipStream_t stream) {
-    const bool few = p.T < kManyTokens || p.K > 16 || p.G > 16;
-    if (!few && p.E <= 64) return start<16, 4, BF16>(p, stream);
-    if (!few && p.E <= 128) return start<16, 8, BF16>(p, stream);
-    if (!few && p.E <= 256) return start<16, 16, BF16>(p, stream);
+    if (p.T >= kManyTokens) {
+        const bool narrow = p.K <= 16 && p.G <= 16;  // slots and groups have a lane each
+        if (narrow && p.E <= 64) return start<16, 4, BF16>(p, stream);
+        if (narrow && p.E <= 128) return start<16, 8, BF16>(p, stream);
+        if (p.G <= 32 && p.E > 128 && p.E <= 256) return start<32, 8, BF16>(p, stream);
+    }
     if (p.E <= 64) return start<64, 1, BF16>(p, stream);
     if (p.E <= 128) return start<64, 2, BF16>(p, stream);
     if (p.E <= 256) return start<64, 4, BF16>(p, stream);
@@ -765,9 +786,11 @@ hipError_t start_route(const RouteParams &p, hipStream_t stream) {
 
 template <bool BF16>
 hipError_t start_backward(const RouteBackwardParams &p, hipStream_t stream) {
-    const bool few = p.T < kManyTokens || p.K > 16;
-    if (!few && p.E <= 64) return start<16, 4, BF16>(p, stream);
-    if (!few && p.E <= 128) return start<16, 8, BF16>(p, stream);
+    if (p.T >= kManyTokens) {
+        if (p.K <= 16 && p.E <= 64) return start<16, 4, BF16>(p, stream);
+        if (p.K <= 16 && p.E <= 128) return start<16, 8, BF16>(p, stream);
+        if (p.E > 128 && p.E <= 256) return start<32, 8, BF16>(p, stream);
+    }
     if (p.E <= 64) return start<64, 1, BF16>(p, stream);
     if (p.E <= 128) return start<64, 2, BF16>(p, stream);
     return start<64, 4, BF16>(p, stream);

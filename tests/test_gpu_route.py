@@ -59,7 +59,8 @@ def test_choice_and_weights(E, kind, dtype, renorm):
         assert status == 0
 
 
-# 2048 tokens and more go 16 lanes to a token, where they hold its experts (256), slots (16) and groups (16)
+# 4096 tokens and more go 16 lanes to a token, where they hold its experts (128), slots (16) and groups (16), or 32
+# (256 experts)
 MANY = [(16, 2, 1, 1), (60, 6, 1, 1), (64, 6, 8, 3), (65, 4, 5, 2), (128, 8, 16, 5), (160, 8, 8, 3), (192, 3, 6, 2),
         (256, 8, 8, 4), (256, 16, 16, 16), (256, 17, 4, 2), (256, 8, 32, 9), (257, 8, 1, 1), (12, 16, 3, 2)]
 
@@ -67,9 +68,9 @@ MANY = [(16, 2, 1, 1), (60, 6, 1, 1), (64, 6, 8, 3), (65, 4, 5, 2), (128, 8, 16,
 @pytest.mark.parametrize("E,k,groups,kept", MANY)
 @pytest.mark.parametrize("kind,dtype,with_bias", [("sigmoid", torch.float32, True), ("softmax", torch.bfloat16, False),
                                                   ("softmax", torch.float32, True), ("sigmoid", torch.bfloat16, True)])
-def test_many_tokens(E, k, groups, kept, kind, dtype, with_bias):
+@pytest.mark.parametrize("T", [2049, 4099])
+def test_many_tokens(E, k, groups, kept, kind, dtype, with_bias, T):
     rng = np.random.default_rng(E + k)
-    T = 2049
     print(f"[route] many tokens E={E} k={k} G={groups} {kind} {dtype} bias={with_bias}", flush=True)
     values, logits = _logits(rng, T, E, dtype)
     bias = (rng.standard_normal(E) * 0.1).astype(np.float32) if with_bias else None
@@ -90,7 +91,7 @@ def test_many_tokens(E, k, groups, kept, kind, dtype, with_bias):
     _check_gradient(out[torch.from_numpy(at).cuda()], values[at], got_i[at], gw[at], kind, kind == "sigmoid", 1.5)
 
 
-@pytest.mark.parametrize("T", [70, 2100])
+@pytest.mark.parametrize("T", [70, 2100, 4100])
 @pytest.mark.parametrize("kind", sorted(KINDS))
 def test_near_ties_among_many_and_few_tokens(T, kind):
     """Biases that undo the scores' differences to a few steps of f32: every token's order is a near tie."""
@@ -109,7 +110,7 @@ def test_near_ties_among_many_and_few_tokens(T, kind):
         _weights_near(got_w[at], want_w, kind, True)
 
 
-@pytest.mark.parametrize("T", [500, 2100])
+@pytest.mark.parametrize("T", [500, 2100, 4100])
 @pytest.mark.parametrize("kind", sorted(KINDS))
 @pytest.mark.parametrize("k", [1, 2, 3])
 def test_near_tie_behind_equal_experts(T, kind, k):
@@ -141,7 +142,8 @@ def test_near_tie_behind_equal_experts(T, kind, k):
     assert np.array_equal(got_i, want_i)
 
 
-@pytest.mark.parametrize("T,E,k", [(130, 200, 8), (130, 200, 32), (2100, 200, 16), (2100, 60, 3), (40, 1500, 8)])
+@pytest.mark.parametrize("T,E,k", [(130, 200, 8), (130, 200, 32), (2100, 200, 16), (2100, 60, 3), (40, 1500, 8), (4100, 60, 3),
+                                   (4100, 120, 16), (4100, 200, 32), (4100, 240, 8)])
 @pytest.mark.parametrize("kind", sorted(KINDS))
 @pytest.mark.parametrize("groups,kept,best", [(1, 1, 1), (10, 4, 2), (20, 7, 1)])
 def test_more_near_ties_than_candidates(T, E, k, kind, groups, kept, best):
@@ -176,7 +178,7 @@ def test_groups(E, groups, kept, best, kind, with_bias):
     _weights_near(got_w, want_w, kind, True)
 
 
-@pytest.mark.parametrize("T", [300, 2100])
+@pytest.mark.parametrize("T", [300, 2100, 4100])
 @pytest.mark.parametrize("kind", sorted(KINDS))
 def test_group_ratings_that_cancel(T, kind):
     """The two best of each group are about 64 and -64: their sum is far smaller than what f32 makes of each is off by."""
@@ -291,7 +293,8 @@ def test_rows_apart(dtype):
 
 
 @pytest.mark.parametrize("dtype", [torch.float32, torch.bfloat16])
-@pytest.mark.parametrize("T,E", [(50, 100), (50, 200), (30, 471), (2100, 61), (2100, 120), (2100, 255), (9, 1501)])
+@pytest.mark.parametrize("T,E", [(50, 100), (50, 200), (30, 471), (2100, 61), (2100, 120), (2100, 255), (9, 1501), (4100, 61), (4100, 120),
+                                 (4100, 255)])
 def test_rows_apart_equal_rows_together(T, E, dtype):
     """Rows that start on any element, of whole and of part lanes: the same bits as rows without gaps."""
     rng = np.random.default_rng(T + E)
@@ -411,7 +414,7 @@ def test_gradient_of_masked_and_bad_logits():
         _check_gradient(out, bad, idx, gw, kind, renorm, 1.0)
 
 
-@pytest.mark.parametrize("T", [40, 2100])
+@pytest.mark.parametrize("T", [40, 2100, 4100])
 def test_gradient_of_tokens_without_slots_reads_no_logits(T):
     """A padded batch: NaN logits where the mask left no slot are neither flagged nor passed on."""
     rng = np.random.default_rng(6)
