@@ -126,7 +126,8 @@ __device__ __forceinline__ void zero_padding(const Params &p) {
 // One block per token: the token's gradient row is scaled into each of its grouped rows, and its
 // product with that row's output summed over the block.  The gradient row stays in registers, UPT
 // 16-byte units a thread (rows of up to 64 WAVES UPT units; longer ones in turns), and the next row's
-// outputs are loaded while one is worked on.
+// outputs are loaded while one is worked on.  Bound by HBM: 16384 tokens of 6 rows of 4096 take 329 us for 1.75
+// GB, 5.3 TB/s; 1000 tokens of 8 rows of 7168 with padding 49 us.
 template <int WAVES, int UPT>
 __global__ __launch_bounds__(WAVES *kWave) void combine_grouped_backward_kernel(Params p) {
     __shared__ float s_dot[kMaxTopk][WAVES];
