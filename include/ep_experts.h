@@ -119,7 +119,8 @@ ep_status_t ep_route_backward(const ep_shape_t *s, const ep_router_t *r, const v
  * The gradient with respect to x's values is the same product of the quantised gradient with the
  * transposed weights: w [num_experts][k][n] and w_scales [num_experts][k / 128][n / 128].
  * Limits: k a positive multiple of 128, n a positive multiple of 8 (EP_ERR_INVALID_ARG); n * k
- * < 2^31, k <= 2^20, num_experts <= 16384, and no more than 2^31 - 1 tiles of work (EP_ERR_UNSUPPORTED).
+ * < 2^31, k <= 2^20, num_experts <= 16384, and a launch of no more than 2^31 - 1 threads, 512 for each part
+ * of a segment of up to 16 rows and each 64 columns at most (EP_ERR_UNSUPPORTED).
  * x, w and out 16-byte, scales and expert_rows 4-byte aligned.  One launch.
  * dev_status (nullable): EP_DEV_RECV_OVERFLOW (the segments pass num_rows: the rows past it are
  * not computed).
