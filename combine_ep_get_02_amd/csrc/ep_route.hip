@@ -710,44 +710,63 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_backward_kernel(Rout
         sum = token_sum<LPT>(sum);
     }
 
-    // lane j: the score of slot j's expert and its gradient, in 64 bits: the sums over the slots cancel
-    double s = 0.0, g = 0.0;
+    // Lane j: what slot j adds to its expert's logit, whole in 64 bits and rounded once.  The gradient of a score
+    // is as large as the score is small, and the sums over the slots cancel: neither part alone fits 32 bits.
+    double s = 0.0, rest = 1.0, g = 0.0;  // the score, 1 - score (a sigmoid's), the weight's gradient
     if (id >= 0) {
         const float l = load_logit<BF16>(p.a.logits, row + id);
-        if (l > -INFINITY && !unusable(l))
-            s = p.sigmoid ? 1.0 / (1.0 + exp(-(double)l)) : exp((double)l - (double)top) / (double)sum;
+        if (l > -INFINITY && !unusable(l)) {
+            if (p.sigmoid) {
+                s = 1.0 / (1.0 + exp(-(double)l));
+                rest = 1.0 / (1.0 + exp((double)l));  // does not cancel where s is near 1
+            } else {
+                s = exp((double)l - (double)top) / (double)sum;
+            }
+        }
         g = p.a.grad_w[t * p.K + at];
     }
-    double ds = g * (double)p.scale;
+    const double scale = (double)p.scale;
+    double part, mean = 0.0;  // mean: sum over the slots of ds s, which every logit of a softmax gets its score's share of
     if (p.renorm) {
-        const double all = token_sum<LPT>(s), gs = token_sum<LPT>(g * s);
-        ds = id >= 0 && all > 0.0 ? (double)p.scale * (g - gs / all) / all : 0.0;
+        const double all = token_sum<LPT>(s), r = all > 0.0 ? s / all : 0.0;
+        part = scale * (g - token_sum<LPT>(g * r)) * r;  // and these have a mean of 0
+    } else {
+        part = scale * g * s;
+        if (!p.sigmoid) {
+            mean = token_sum<LPT>(part);
+            bool first = true;  // an expert named by several slots gets the mean's share once
+            for (int j = 0; j < p.K; ++j) {
+                const int e = LPT == kWave ? readlane32(id, j) : __shfl(id, base + j);
+                first = first && !(j < at && e == id);
+            }
+            if (first) part -= mean * s;
+        }
     }
-    const float slot = (float)ds;
-    const float mean = p.sigmoid ? 0.0f : (float)token_sum<LPT>(ds * s);
+    const float slot = (float)(part * rest);
+    const bool everywhere = !p.sigmoid && !p.renorm;  // experts without a slot have a gradient too
+    const float share = (float)mean;
 
     for (int from = 0; from < p.E; from += kSpan) {
         if (p.E > kSpan) load(from);
         const int e0 = from + at * VPL;
         float d[VPL];
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) d[i] = 0.0f;
+        for (int i = 0; i < VPL; ++i) d[i] = everywhere ? -(expf(logit[i] - top) / sum * share) : 0.0f;
+        uint32_t named = 0;
         for (int j = 0; j < p.K; ++j) {
             const int e = (LPT == kWave ? readlane32(id, j) : __shfl(id, base + j)) - e0;
             const float v = LPT == kWave ? readlanef(slot, j) : __shfl(slot, base + j);
 #pragma unroll
-            for (int i = 0; i < VPL; ++i)
-                if (e == i) d[i] += v;
+            for (int i = 0; i < VPL; ++i) {
+                if (e == i) {
+                    d[i] = (named >> i & 1u) != 0u ? d[i] + v : v;
+                    named |= 1u << i;
+                }
+            }
         }
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) {
-            // sigmoid: 1 - s as its own sigmoid, which does not cancel where s is near 1
-            if (p.sigmoid)
-                d[i] = d[i] * (1.0f / (1.0f + expf(-logit[i]))) * (1.0f / (1.0f + expf(logit[i])));
-            else
-                d[i] = expf(logit[i] - top) / sum * (d[i] - mean);
+        for (int i = 0; i < VPL; ++i)
             if (logit[i] == -INFINITY) d[i] = 0.0f;
-        }
         if (!here) continue;
         const int64_t out = t * p.a.grad_stride + e0;
         store_logits<VPL, BF16>(p.a.grad_logits, out, p.E - e0, d);
