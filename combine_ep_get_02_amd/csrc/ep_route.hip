@@ -686,10 +686,11 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_backward_kernel(Rout
             }
         }
     };
-    // softmax: the largest logit and the sum relative to it
+    // a softmax that is not renormalised: the largest logit and the sum relative to it
+    const bool whole_row = !p.sigmoid && !p.renorm;
     float top = 0.0f, sum = 1.0f;
     load(0);
-    if (!p.sigmoid) {
+    if (whole_row) {
         int m = kNone;
         for (int from = 0; from < p.E; from += kSpan) {
             if (from > 0) load(from);
@@ -713,17 +714,24 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_backward_kernel(Rout
     // Lane j: what slot j adds to its expert's logit, whole in 64 bits and rounded once.  The gradient of a score
     // is as large as the score is small, and the sums over the slots cancel: neither part alone fits 32 bits.
     double s = 0.0, rest = 1.0, g = 0.0;  // the score, 1 - score (a sigmoid's), the weight's gradient
+    float l = -INFINITY;
     if (id >= 0) {
-        const float l = load_logit<BF16>(p.a.logits, row + id);
-        if (l > -INFINITY && !unusable(l)) {
-            if (p.sigmoid) {
-                s = 1.0 / (1.0 + exp(-(double)l));
-                rest = 1.0 / (1.0 + exp((double)l));  // does not cancel where s is near 1
-            } else {
-                s = exp((double)l - (double)top) / (double)sum;
-            }
-        }
+        l = load_logit<BF16>(p.a.logits, row + id);
+        if (unusable(l)) l = -INFINITY;
         g = p.a.grad_w[t * p.K + at];
+    }
+    double ref = (double)top;
+    if (!p.sigmoid && p.renorm) {  // only the ratios of the chosen ones' scores count
+        const int m = token_max<LPT>(l > -INFINITY ? order_of(l) : kNone);
+        ref = m == kNone ? 0.0 : (double)value_of(m);
+    }
+    if (l > -INFINITY) {
+        if (p.sigmoid) {
+            s = 1.0 / (1.0 + exp(-(double)l));
+            rest = 1.0 / (1.0 + exp((double)l));  // does not cancel where s is near 1
+        } else {
+            s = exp((double)l - ref) / (double)sum;
+        }
     }
     const double scale = (double)p.scale;
     double part, mean = 0.0;  // mean: sum over the slots of ds s, which every logit of a softmax gets its score's share of
@@ -732,7 +740,7 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_backward_kernel(Rout
         part = scale * (g - token_sum<LPT>(g * r)) * r;  // and these have a mean of 0
     } else {
         part = scale * g * s;
-        if (!p.sigmoid) {
+        if (whole_row) {
             mean = token_sum<LPT>(part);
             bool first = true;  // an expert named by several slots gets the mean's share once
             for (int j = 0; j < p.K; ++j) {
@@ -743,7 +751,6 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_backward_kernel(Rout
         }
     }
     const float slot = (float)(part * rest);
-    const bool everywhere = !p.sigmoid && !p.renorm;  // experts without a slot have a gradient too
     const float share = (float)mean;
 
     for (int from = 0; from < p.E; from += kSpan) {
@@ -751,7 +758,8 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_backward_kernel(Rout
         const int e0 = from + at * VPL;
         float d[VPL];
 #pragma unroll
-        for (int i = 0; i < VPL; ++i) d[i] = everywhere ? -(expf(logit[i] - top) / sum * share) : 0.0f;
+        for (int i = 0; i < VPL; ++i)  // experts without a slot have a gradient there too
+            d[i] = whole_row ? -(expf(logit[i] - top) / sum * share) : 0.0f;
         uint32_t named = 0;
         for (int j = 0; j < p.K; ++j) {
             const int e = (LPT == kWave ? readlane32(id, j) : __shfl(id, base + j)) - e0;

@@ -59,8 +59,10 @@ typedef struct {
  *           of the highest rating stay, ties to the lower group
  *   top k   the num_topk experts of the largest c_e in the groups kept, in descending order,
  *           ties to the lower expert
- *   weight  w_j = weight_scale * s_{e_j}, divided by the sum of the token's chosen s when
- *           renormalize is set (0 when that sum is 0)
+ *   weight  w_j = weight_scale * s_{e_j}, divided by the sum S of the token's chosen s when
+ *           renormalize is set.  A softmax's s_{e_j} / S are formed from the chosen logits alone,
+ *           however far they are below the row's largest; a sigmoid's are 0 when every chosen s
+ *           is 0 in binary64 (logits below about -709)
  * Choices and ratings compare as in binary64, so near ties are decided as the definition does; the
  * weights are rounded to f32 once.  An expert is eligible unless its logit is -inf (a masked
  * expert) or its bias is -inf, or either is NaN or +inf (flagged, EP_DEV_BAD_LOGIT); such an
@@ -82,10 +84,12 @@ ep_status_t ep_route(const ep_shape_t *s, const ep_router_t *r, const void *logi
 /*
  * Gradient of ep_route's weights with respect to the logits; the choice itself has none.  With
  * the token's slots j that hold an expert e_j, S = sum of s_{e_j} and g_j = grad_weights[t][j]:
- *   ds_j = weight_scale * (g_j - sum_i g_i s_{e_i} / S) / S   when renormalize is set (0 if S is 0)
+ *   ds_j = weight_scale * (g_j - sum_i g_i s_{e_i} / S) / S   when renormalize is set
  *   ds_j = weight_scale * g_j                                 otherwise
  *   grad_logits[t][e] = s_e (1 - s_e) * (sum of ds_j over the slots naming e)          sigmoid
  *   grad_logits[t][e] = s_e * (sum of ds_j over the slots naming e - sum_j ds_j s_{e_j})  softmax
+ * Each slot's part is formed in binary64 (ds_j is as large as S is small, and is not rounded by
+ * itself), with s_{e_j} / S as for the weights: 0 where those are.
  * Slots of -1 have no part (a token whose slots are all -1 gets a row of zeros, and its logits are
  * not read); an expert named by several slots gets the sum.  A logit that is not finite gets 0.
  * In:  logits as ep_route took them; topk_idx [t][k] as it wrote them; grad_weights [t][k] f32.

@@ -139,3 +139,61 @@ def test_gradient_of_an_expert_in_several_slots(kind, renorm):
         idx[:16, 4] = idx[:16, 1]
         gw = rng.standard_normal((T, k)).astype(np.float32)
         _check(_backward(logits, idx, gw, kind, renorm, 1.5), values, idx, gw, kind, renorm, 1.5)
+
+
+@pytest.mark.parametrize("T,E,k", SIZES)
+@pytest.mark.parametrize("below", [300.0, 800.0, 1e6, 1e37])
+@pytest.mark.parametrize("renorm", [True, False])
+def test_softmax_weights_and_gradient_agree_however_far_below_the_top(T, E, k, below, renorm):
+    """A bias picks experts whose scores binary64 cannot hold: renormalised weights are ratios to each other, and the
+    gradient is that of these ratios; others are 0, and so is their gradient."""
+    rng = np.random.default_rng(E)
+    values, _, idx = _case(rng, T, E, k, 0.0, torch.float32)
+    values[np.arange(T)[:, None], idx] -= np.float32(below)
+    # the same experts in every token, so that a bias can pick them
+    values[:, idx[0]] = np.float32(-below) * (1 + rng.integers(0, 2, (T, k)) * 2.0 ** -23) - rng.random((T, k)).astype(np.float32)
+    rest = np.setdiff1d(np.arange(E), idx[0])
+    values[:, rest] = rng.standard_normal((T, len(rest)))
+    values = values.astype(np.float32)
+    bias = np.zeros(E, np.float32)
+    bias[idx[0]] = 2.0 + np.arange(k)  # in this order: scores are 0 and 1 at most
+    logits = torch.from_numpy(values).cuda()
+    got_i = torch.empty(T, k, dtype=torch.int64, device="cuda")
+    got_w = torch.empty(T, k, device="cuda")
+    experts.ep_route(ep.make_shape(T, 8, k, E, 1, 1), experts.make_router(0, 1, 1, 1, renorm, 2.5), logits,
+                     torch.from_numpy(bias).cuda(), None, got_i, got_w)
+    order = np.repeat(idx[:1, ::-1], T, 0)
+    assert np.array_equal(got_i.cpu().numpy(), order)
+    chosen = np.take_along_axis(values.astype(np.float64), order, 1)
+    r = np.exp(chosen - chosen.max(1, keepdims=True))
+    r /= r.sum(1, keepdims=True)
+    if not renorm:
+        r = np.exp(_log_scores(values, "softmax")[0])[np.arange(T)[:, None], order]
+    # formed in binary64 and rounded once, but for a sum of f32 exponentials, 56 U
+    assert np.all(np.abs(got_w.double().cpu().numpy() - 2.5 * r) <= (2 if renorm else 58) * U * 2.5 * r + 2.0 ** -149)
+    gw = rng.standard_normal((T, k)).astype(np.float32)
+    at = np.unique(np.concatenate([np.arange(min(T, 30)), [T - 1]]))
+    out = _backward(logits, order, gw, "softmax", renorm, 2.5)
+    _check(out[torch.from_numpy(at).cuda()], values[at], order[at], gw[at], "softmax", renorm, 2.5)
+
+
+@pytest.mark.parametrize("level", [-705.0, -800.0, -1e30])
+def test_sigmoid_weights_and_gradient_where_scores_end(level):
+    """Below about -709 a sigmoid is 0 in binary64: weights and gradient are 0; above, both are those of the ratios."""
+    rng = np.random.default_rng(3)
+    T, E, k = 20, 16, 3
+    values = np.full((T, E), -1e35, np.float32)
+    idx = np.stack([np.sort(rng.choice(E, k, replace=False)) for _ in range(T)]).astype(np.int64)
+    np.put_along_axis(values, idx, np.float32(level) - np.arange(k, dtype=np.float32), 1)
+    logits = torch.from_numpy(values).cuda()
+    got_i, got_w = torch.empty(T, k, dtype=torch.int64, device="cuda"), torch.empty(T, k, device="cuda")
+    experts.ep_route(ep.make_shape(T, 8, k, E, 1, 1), experts.make_router(1, 1, 1, 1, True, 1.0), logits, None, None, got_i, got_w)
+    assert np.array_equal(got_i.cpu().numpy(), idx)
+    gw = rng.standard_normal((T, k)).astype(np.float32)
+    out = _backward(logits, idx, gw, "sigmoid", True, 1.0)
+    if level < -709:
+        assert not got_w.any() and not out.any()
+        return
+    r = np.exp(-np.arange(k))
+    assert np.all(np.abs(got_w.double().cpu().numpy() - r / r.sum()) <= 2 * U * r / r.sum())
+    _check(out, values, idx, gw, "sigmoid", True, 1.0)
