@@ -538,6 +538,7 @@ __global__ __launch_bounds__(NG *KS *kWave, WAVES) void expert_gemm_narrow_kerne
         for (int i = 0; i < WL; ++i) tile[i * kWave + lane] = c.w[i];
 #pragma unroll
         for (int i = 0; i < XL; ++i) tile[(WL + i) * kWave + lane] = c.x[i];
+        wave_lds_order();
         u32x4 x[MF][2];
 #pragma unroll
         for (int i = 0; i < MF; ++i) {
@@ -573,6 +574,7 @@ __global__ __launch_bounds__(NG *KS *kWave, WAVES) void expert_gemm_narrow_kerne
                 for (int e = 0; e < 4; ++e) acc[i][j][e] = __builtin_fmaf(part[e], s, acc[i][j][e]);
             }
         }
+        wave_lds_order();  // the next tile, or the sums, go where this one was
     };
     Codes c[DEEP];
 #pragma unroll

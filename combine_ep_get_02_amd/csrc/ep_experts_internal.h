@@ -86,6 +86,13 @@ hipError_t start_kernel(void (*kernel)(A...), int64_t blocks, int threads, hipSt
     return e;
 }
 
+// Orders LDS accesses of the wave's own lanes among each other (they are served in order, but
+// the compiler does not know that one lane's stores are for another's loads).
+__device__ __forceinline__ void wave_lds_order() {
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront", "local");
+    __builtin_amdgcn_wave_barrier();
+}
+
 // Two f32 to a pair of bf16 in one word, nearest, ties to even, NaN kept (v_cvt_pk_bf16_f32).
 __device__ __forceinline__ uint32_t pack_bf16(float lo, float hi) {
     typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));

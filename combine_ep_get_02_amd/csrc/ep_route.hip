@@ -140,12 +140,6 @@ __device__ __forceinline__ void store_logits(void *p, int64_t i, int left, const
     }
 }
 
-// Orders LDS accesses of the wave's own lanes among each other (they are served in order).
-__device__ __forceinline__ void wave_lds_order() {
-    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
-    __builtin_amdgcn_wave_barrier();
-}
-
 // NaN and +inf: not a logit (or bias) the router can use.
 __device__ __forceinline__ bool unusable(float v) { return !(v < INFINITY); }
 
