@@ -742,8 +742,11 @@ bool gemm_grid_ok(const GemmArgs &a) {
 
 hipError_t launch_expert_gemm(const GemmArgs &a, hipStream_t stream) {
     const Plan pl = plan(a);
-    const int64_t blocks = grid_blocks(a, pl);
-    if (blocks == 0) return hipSuccess;
+    int64_t blocks = grid_blocks(a, pl);
+    if (blocks == 0) {  // no rows: nothing but sizes that say there are some
+        if (a.expert_rows == nullptr || a.dev_status == nullptr) return hipSuccess;
+        blocks = 1;
+    }
     return start_kernel(pl.kernel, blocks, pl.threads, stream, a, (a.n + pl.cols - 1) / pl.cols);
 }
 

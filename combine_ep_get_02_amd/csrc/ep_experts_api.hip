@@ -36,12 +36,13 @@ ep_status_t gemm_checked(const GemmArgs &a) {
     if ((int64_t)a.n * (a.swiglu ? 2 : 1) * a.k > INT_MAX || a.k > kMaxGemmK || a.num_experts > kMaxGemmExperts)
         return EP_ERR_UNSUPPORTED;
     if (!gemm_grid_ok(a)) return EP_ERR_UNSUPPORTED;
+    if (!aligned(a.expert_rows, 4)) return EP_ERR_INVALID_ARG;
     if (a.num_rows == 0) return EP_OK;
     if (a.x == nullptr || a.x_scales == nullptr || a.w == nullptr || a.w_scales == nullptr || a.out == nullptr ||
         (a.swiglu && a.out_scales == nullptr))
         return EP_ERR_INVALID_ARG;
     if (!aligned(a.x, 16) || !aligned(a.w, 16) || !aligned(a.out, 16) || !aligned(a.x_scales, 4) ||
-        !aligned(a.w_scales, 4) || !aligned(a.out_scales, 4) || !aligned(a.expert_rows, 4))
+        !aligned(a.w_scales, 4) || !aligned(a.out_scales, 4))
         return EP_ERR_INVALID_ARG;
     return EP_OK;
 }
@@ -130,7 +131,7 @@ ep_status_t ep_expert_gemm_fp8(int32_t num_experts, int32_t n, int32_t k, const 
     a.out = out;
     a.dev_status = dev_status;
     const ep_status_t st = gemm_checked(a);
-    if (st != EP_OK || num_rows == 0) return st;
+    if (st != EP_OK) return st;
     return from_hip(launch_expert_gemm(a, stream));
 }
 
@@ -153,7 +154,7 @@ ep_status_t ep_expert_gemm_swiglu_fp8(int32_t num_experts, int32_t n, int32_t k,
     a.dev_status = dev_status;
     a.swiglu = true;
     const ep_status_t st = gemm_checked(a);
-    if (st != EP_OK || num_rows == 0) return st;
+    if (st != EP_OK) return st;
     return from_hip(launch_expert_gemm(a, stream));
 }
 

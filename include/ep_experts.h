@@ -125,9 +125,10 @@ ep_status_t ep_route_backward(const ep_shape_t *s, const ep_router_t *r, const v
  * Limits: k a positive multiple of 128, n a positive multiple of 8 (EP_ERR_INVALID_ARG); n * k
  * < 2^31, k <= 2^20, num_experts <= 16384, and a launch of no more than 2^31 - 1 threads, 512 for each part
  * of a segment of up to 16 rows and each 64 columns at most (EP_ERR_UNSUPPORTED).
- * x, w and out 16-byte, scales and expert_rows 4-byte aligned.  One launch.
- * dev_status (nullable): EP_DEV_RECV_OVERFLOW (the segments pass num_rows: the rows past it are
- * not computed).
+ * x, w and out 16-byte, scales and expert_rows 4-byte aligned.  One launch (with no rows only where
+ * there are sizes to look at and a status to set).
+ * dev_status (nullable): EP_DEV_RECV_OVERFLOW (the segments pass num_rows, which may be 0: the rows
+ * past it are not computed).
  */
 ep_status_t ep_expert_gemm_fp8(int32_t num_experts, int32_t n, int32_t k, const void *x, const float *x_scales,
                                const void *w, const float *w_scales, const int32_t *expert_rows, int32_t num_rows,
