@@ -7,15 +7,12 @@
 // hold these).  The weights are the A operand and the rows the B operand, so a lane's results are
 // neighbouring columns of one row: one scale a lane and contiguous stores.
 //
-// Two kinds of matrix instruction serve:
-//   - bf16 outputs take the E4M3 instructions, at twice the f16 rate.  They add the eight products of
-//     a group of neighbouring channels with 13 bits below the largest one's, the rest of a product
-//     being cut (measured: 2^8 keeps 2^-5 of its group and loses 2^-6), and the groups in f32.
-//     Against f32 that is 1.5e-5 of the result for normally distributed codes, a hundredth of the
-//     rounding to bf16 that follows.
-//   - the SwiGLU form's scales leave in f32, where 1.5e-5 would show.  It takes the f16 instructions
-//     on codes turned into f16 (exact: every E4M3 value is one, and a product of two fits f32), whose
-//     sums are f32 throughout (measured 1e-8).
+// The codes are turned into f16 for the f16 matrix instructions (exact: every E4M3 value is one, and a
+// product of two fits f32), whose sums are f32 throughout (measured: 1e-8 of normally distributed codes'
+// result).  The E4M3 instructions run at twice the rate, but add the eight products of a group of
+// neighbouring channels with 13 bits below the largest one's and cut the rest of each (measured: 2^8
+// keeps 2^-5 of its group and loses 2^-6): one channel at 448 * 448 would take away what its seven
+// neighbours add below 24.5.
 #include <limits.h>
 
 #include "ep_experts_internal.h"
@@ -24,7 +21,6 @@ namespace ep {
 namespace {
 
 typedef unsigned int u32x4 __attribute__((ext_vector_type(4)));
-typedef int i32x8 __attribute__((ext_vector_type(8)));
 typedef float f32x4 __attribute__((ext_vector_type(4)));
 typedef float f32x16 __attribute__((ext_vector_type(16)));
 
@@ -100,11 +96,6 @@ __device__ __forceinline__ f16x8 to_f16(u32x4 unit) {
     return f;
 }
 
-// Two units of codes as one operand of a matrix instruction on codes.
-__device__ __forceinline__ i32x8 codes(u32x4 lo, u32x4 hi) {
-    return i32x8{(int)lo[0], (int)lo[1], (int)lo[2], (int)lo[3], (int)hi[0], (int)hi[1], (int)hi[2], (int)hi[3]};
-}
-
 // Buffer descriptor over `bytes` bytes from p; loads past them return 0.
 __device__ __forceinline__ __amdgpu_buffer_rsrc_t descriptor(const void *p, uint32_t bytes) {
     return __builtin_amdgcn_make_buffer_rsrc(const_cast<void *>(p), 0, (int)bytes, 0x00027000);
@@ -141,28 +132,27 @@ __device__ __forceinline__ int rotate(int r, int c) { return c ^ ((r ^ ((r >> 3)
 constexpr int kBN = 256;  // weight rows of a wide block
 
 // Many rows: 64 MI rows x 256 weight rows a block, 2 x 4 waves of 32 MI rows x 64 weight rows.  A block of 128
-// channels of both goes straight to LDS, two or three steps' worth at a time; its products are summed by the
-// matrix instructions and scaled into the wave's sums by one FMA each (a scale covers 128 channels).  The scaled
-// sums have to be in registers that vector instructions reach, which bounds a wave at 128 x 64 results.
+// channels of both goes straight to LDS, two steps ahead; its products are summed by the matrix instructions and
+// scaled into the wave's sums by one FMA each (a scale covers 128 channels).  The scaled sums have to be in
+// registers that vector instructions reach.
 //
-// Product of 32768 rows of 32 experts, 2048 channels to 7168: 583 us, 1.65 PFLOP/s.  The E4M3 instructions are 40%
-// of the time at work, and without any one part it is faster (of 633 us on a warm card: loads 481, LDS reads 556,
-// scaling 593, stores 591).  SwiGLU of as many rows, 7168 to 2048: 1900 us, 1.01 PFLOP/s with f16 instructions, at
-// the power limit: those, the conversion and the LDS reads alone reach 1.55 on such data.
+// Bound by the f16 matrix instructions, the conversions to f16 and the LDS reads that feed them: those three alone
+// reach 1.55 PFLOP/s on such data, the instructions alone 1.82.  SwiGLU of 32768 rows of 32 experts, 7168 channels
+// to 2048: 1920 us, 1.00 PFLOP/s; product of as many rows, 2048 channels to 7168: 1040 us, 0.93.  (The E4M3
+// instructions took the product in 606 us, without the sums' last bits.)
 template <bool SWIGLU, int MI>
 __global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(GemmArgs p, int col_tiles) {
     constexpr int WM = 2, WN = 4, BM = 32 * MI * WM, HALF = 32;
     static_assert(2 * HALF * WN == kBN, "256 weight rows a block");
     constexpr int XL = BM * kUnits / kBlockThreads, WL = kBN * kUnits / kBlockThreads;  // units a thread loads
-    // STAGES buffers: while one block of channels is multiplied the next ones are on their way.  A
+    // Three buffers: while one block of channels is multiplied the next two are on their way.  A
     // wave's last load of a step is of scales: rows' by the first BM lanes, the weights' two by the
     // lanes of the next wave (the others repeat those).  (One array a buffer: the compiler tells them
     // apart, and would wait for all loads before a read of an array that it does not.)
-    constexpr int STAGES = MI == 4 ? 2 : 3;
     constexpr int kLoads = XL + WL + 1;  // of a wave and step
     static_assert(BM <= 64 * (WM * WN - 1), "a wave is left for the weights' scales");
     constexpr int kX = 0, kW = BM * kUnits, kS = kW + kBN * kUnits, kBuffer = kS + kBlockThreads / 4;
-    __shared__ u32x4 s_0[kBuffer], s_1[kBuffer], s_2[STAGES == 3 ? kBuffer : 1];
+    __shared__ u32x4 s_0[kBuffer], s_1[kBuffer], s_2[kBuffer];
     const int lane = threadIdx.x & (kWave - 1);
     const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
     const int wm = wave / WN, wn = wave % WN;
@@ -246,128 +236,56 @@ __global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(Gemm
     };
     load(s_0, 0);
     load(s_1, 1);
-    if constexpr (SWIGLU) {
-        static_assert(STAGES == 3, "a block is loaded two steps ahead");
+    end_step<kLoads>();
+    auto multiply = [&](const u32x4 *from) {
+        const u32x4 *x = from + kX, *w = from + kW;
+        int u0 = unit0;
+        asm volatile("" : "+v"(u0));  // addresses are cheaper formed anew than kept in registers
+        auto unit_of = [&](const u32x4 *rows, int r, int u) { return rows[r * kUnits + (u0 ^ (2 * u))]; };
+        f16x8 fw[2][8];  // the wave's weights
+#pragma unroll
+        for (int j = 0; j < 2; ++j) {
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const u32x4 unit = unit_of(w, wn * 64 + j * 32 + r32, u);
+                fw[j][2 * u] = to_f16<0>(unit);
+                fw[j][2 * u + 1] = to_f16<1>(unit);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < MI; ++i) {
+            f32x16 part[2] = {};
+#pragma unroll
+            for (int u = 0; u < 4; ++u) {
+                const u32x4 unit = unit_of(x, wm * 32 * MI + i * 32 + r32, u);
+                const f16x8 a = to_f16<0>(unit), b = to_f16<1>(unit);
+                part[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fw[0][2 * u], a, part[0], 0, 0, 0);
+                part[1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fw[1][2 * u], a, part[1], 0, 0, 0);
+                part[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fw[0][2 * u + 1], b, part[0], 0, 0, 0);
+                part[1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fw[1][2 * u + 1], b, part[1], 0, 0, 0);
+            }
+            float scale[2];
+            scales_of(from, i, scale);
+            add(acc[i][0], part[0], scale[0]);
+            add(acc[i][1], part[1], scale[1]);
+        }
+    };
+    // one block of channels: start the loads of the second next, multiply, let the next one's land
+    auto step = [&](const u32x4 *now, u32x4 *later, int b) {
+        load(later, b + 2);
+        if (busy) multiply(now);
         end_step<kLoads>();
-        auto multiply = [&](const u32x4 *from) {
-            const u32x4 *x = from + kX, *w = from + kW;
-            int u0 = unit0;
-            asm volatile("" : "+v"(u0));  // addresses are cheaper formed anew than kept in registers
-            auto unit_of = [&](const u32x4 *rows, int r, int u) { return rows[r * kUnits + (u0 ^ (2 * u))]; };
-            f16x8 fw[2][8];  // the wave's weights
-#pragma unroll
-            for (int j = 0; j < 2; ++j) {
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const u32x4 unit = unit_of(w, wn * 64 + j * 32 + r32, u);
-                    fw[j][2 * u] = to_f16<0>(unit);
-                    fw[j][2 * u + 1] = to_f16<1>(unit);
-                }
-            }
-#pragma unroll
-            for (int i = 0; i < MI; ++i) {
-                f32x16 part[2] = {};
-#pragma unroll
-                for (int u = 0; u < 4; ++u) {
-                    const u32x4 unit = unit_of(x, wm * 32 * MI + i * 32 + r32, u);
-                    const f16x8 a = to_f16<0>(unit), b = to_f16<1>(unit);
-                    part[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fw[0][2 * u], a, part[0], 0, 0, 0);
-                    part[1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fw[1][2 * u], a, part[1], 0, 0, 0);
-                    part[0] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fw[0][2 * u + 1], b, part[0], 0, 0, 0);
-                    part[1] = __builtin_amdgcn_mfma_f32_32x32x16_f16(fw[1][2 * u + 1], b, part[1], 0, 0, 0);
-                }
-                float scale[2];
-                scales_of(from, i, scale);
-                add(acc[i][0], part[0], scale[0]);
-                add(acc[i][1], part[1], scale[1]);
-            }
-        };
-        // one block of channels: start the loads of the second next, multiply, let the next one's land
-        auto step = [&](const u32x4 *now, u32x4 *later, int b) {
-            load(later, b + 2);
-            if (busy) multiply(now);
-            end_step<kLoads>();
-        };
-        // (three steps a turn and no way round any of them: else the compiler would find loads under way
-        // that no path has there, and wait for them)
-        int b = 0;
-        for (; b + 3 <= blocks; b += 3) {
-            step(s_0, s_2, b);
-            step(s_1, s_0, b + 1);
-            step(s_2, s_1, b + 2);
-        }
-        if (b < blocks) step(s_0, s_2, b);
-        if (b + 1 < blocks) step(s_1, s_0, b + 1);
-    } else {
-        static_assert(MI % 2 == 0, "rows alternate between two sets of registers");
-        i32x8 cw[2][2], cx[2][2];  // codes of the weights; of the rows in hand and of the next
-        f32x16 part[2];
-        float scale[2];
-        auto read = [&](const u32x4 *rows, i32x8 (&to)[2]) {
-#pragma unroll
-            for (int h = 0; h < 2; ++h)
-                to[h] = codes(rows[r32 * kUnits + (unit0 ^ (4 * h))], rows[r32 * kUnits + (unit0 ^ (4 * h + 2))]);
-        };
-        auto read_rows = [&](const u32x4 *from, int i) {
-            read(from + kX + (wm * MI + i) * 32 * kUnits, cx[i & 1]);
-            float both[2];
-            scales_of(from, i, both);
-            scale[i & 1] = both[0];
-        };
-        auto product = [&](int i, int j) {
-            const f32x16 zero = {};
-            part[j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(cw[j][0], cx[i & 1][0], zero, 0, 0, 0, 0, 0, 0);
-            part[j] = __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(cw[j][1], cx[i & 1][1], part[j], 0, 0, 0, 0, 0, 0);
-        };
-        // A block of channels is MI times 32 rows by 2 times 32 weight rows.  While one product runs the
-        // one before it is scaled and added and the next rows are read; the last rows' products come
-        // behind the barrier, so that they hide the first reads of the next block.
-        float keep = 0.0f;  // scale of part[1], which is added behind the next product
-        part[1] = f32x16{};
-        auto step = [&](u32x4 *now, const u32x4 *next, int b) {
-#pragma unroll
-            for (int i = 0; i < MI; ++i) {
-                if (i + 1 < MI) {
-                    if (busy) read_rows(now, i + 1);
-                } else {
-                    end_step<(STAGES - 2) * kLoads>();
-                    load(now, b + STAGES);
-                    if (busy) read_rows(next, 0);
-                }
-                if (busy) {
-                    __builtin_amdgcn_sched_barrier(0);
-                    product(i, 0);
-                    __builtin_amdgcn_sched_barrier(0);
-                    add(acc[(i + MI - 1) % MI][1], part[1], keep);
-                    if (i + 1 == MI) read(next + kW + wn * 64 * kUnits, cw[0]);
-                    __builtin_amdgcn_sched_barrier(0);
-                    product(i, 1);
-                    __builtin_amdgcn_sched_barrier(0);
-                    keep = scale[i & 1];
-                    add(acc[i][0], part[0], keep);
-                    if (i + 1 == MI) read(next + kW + (wn * 64 + 32) * kUnits, cw[1]);
-                    __builtin_amdgcn_sched_barrier(0);
-                }
-            }
-        };
-        if constexpr (STAGES == 3) load(s_2, 2);
-        end_step<(STAGES - 1) * kLoads>();
-        if (busy) {
-            read_rows(s_0, 0);
-            read(s_0 + kW + wn * 64 * kUnits, cw[0]);
-            read(s_0 + kW + (wn * 64 + 32) * kUnits, cw[1]);
-        }
-        int b = 0;
-        for (; b + STAGES <= blocks; b += STAGES) {  // no way round a step: as above
-            step(s_0, s_1, b);
-            step(s_1, STAGES == 3 ? s_2 : s_0, b + 1);
-            if constexpr (STAGES == 3) step(s_2, s_0, b + 2);
-        }
-        if (b < blocks) step(s_0, s_1, b);
-        if constexpr (STAGES == 3)
-            if (b + 1 < blocks) step(s_1, s_2, b + 1);
-        add(acc[MI - 1][1], part[1], keep);
+    };
+    // (three steps a turn and no way round any of them: else the compiler would find loads under way
+    // that no path has there, and wait for them)
+    int b = 0;
+    for (; b + 3 <= blocks; b += 3) {
+        step(s_0, s_2, b);
+        step(s_1, s_0, b + 1);
+        step(s_2, s_1, b + 2);
     }
+    if (b < blocks) step(s_0, s_2, b);
+    if (b + 1 < blocks) step(s_1, s_0, b + 1);
 
     // The lane's element e of a 32 x 32 result: row r32, weight row 8 (e / 4) + 4 half + e % 4.  A
     // direct store would put 16 bytes into each of 32 rows; results go through LDS instead and out as
@@ -547,27 +465,20 @@ __global__ __launch_bounds__(NG *KS *kWave, WAVES) void expert_gemm_narrow_kerne
         }
 #pragma unroll
         for (int j = 0; j < WF; ++j) {
-            const u32x4 w[2] = {unit_of(j * 16, 0), unit_of(j * 16, 1)};
             f16x8 fw[4];
-            if constexpr (SWIGLU) {
 #pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    fw[2 * h] = to_f16<0>(w[h]);
-                    fw[2 * h + 1] = to_f16<1>(w[h]);
-                }
+            for (int h = 0; h < 2; ++h) {
+                const u32x4 w = unit_of(j * 16, h);
+                fw[2 * h] = to_f16<0>(w);
+                fw[2 * h + 1] = to_f16<1>(w);
             }
 #pragma unroll
             for (int i = 0; i < MF; ++i) {
                 f32x4 part = {0.f, 0.f, 0.f, 0.f};
-                if constexpr (SWIGLU) {
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) {
-                        part = __builtin_amdgcn_mfma_f32_16x16x32_f16(fw[2 * h], to_f16<0>(x[i][h]), part, 0, 0, 0);
-                        part = __builtin_amdgcn_mfma_f32_16x16x32_f16(fw[2 * h + 1], to_f16<1>(x[i][h]), part, 0, 0, 0);
-                    }
-                } else {
-                    part = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(codes(w[0], w[1]), codes(x[i][0], x[i][1]),
-                                                                            part, 0, 0, 0, 0, 0, 0);
+                for (int h = 0; h < 2; ++h) {
+                    part = __builtin_amdgcn_mfma_f32_16x16x32_f16(fw[2 * h], to_f16<0>(x[i][h]), part, 0, 0, 0);
+                    part = __builtin_amdgcn_mfma_f32_16x16x32_f16(fw[2 * h + 1], to_f16<1>(x[i][h]), part, 0, 0, 0);
                 }
                 const float s = c.sx[i] * c.sw[SWIGLU && j >= SETS];
 #pragma unroll
@@ -680,20 +591,21 @@ Plan narrow() {
 //            s 2, 4, 4, 2 170  168  170  172  217  229
 //            wide 64      163  163  163  164  165  168  175  237  297  388  532  664 1181
 //            wide 128     168  168  168  169  169  173  173  219  248  388  477  601 1051
-//   product  s 1, 4, 1, 8  80   83   88   98  120  134
-//            s 2, 4, 1, 8 105  111  110  113  122  145
-//            s 2, 4, 2, 2  86   91   92   92   96  111  128
-//            wide 128     101  101  103  104  105  104  104  105  107  138  169  210  364
-//            wide 256     118  121  120  119  120  119  120  121  125  137  151  198  334
+//   product  s 1, 4, 1, 8  81   83   87   97  119  135  174  215
+//            s 2, 4, 1, 8 112  116  116  117  126  152  196  237
+//            s 2, 4, 2, 2  86   89   88   90   97  109  127  148  194
+//            wide 64       96   94   99   99   99  101  107  124  157  200  283  345  636
+//            wide 128     104  104  105  105  106  107  107  137  143  181  247  297  549
 // Where there are fewer blocks than compute units a block's own time counts, and more waves of a block
 // on the channels, or fewer columns a block, shorten it.  One expert, product of 7168 channels to 2048
 // and of 2048 to 7168, and SwiGLU of 7168 to 2048, us:
-//   rows                    1   16   64  128  256  512 1024 2048 4096 |   1   64  128  256 1024 2048 4096
-//   product  s 1, 1, 1, 8   6    8   13   24   44                     |   6   20   36
-//            s 1, 4, 1, 8   9   11   11   13   20   34   65           |   6    9   15   24
-//            s 2, 4, 1, 8  11   13   15   15   16   28   54  105      |   7    8   13   25   79
-//            wide 128      34   35   36   55   55   56   57   61   75 |  13   14   20   20   23   44   92
-//            wide 256      57   57   59   63   95   95   95   98  101 |  21   21   22   31   33   38   76
+//   rows                    1   16   64  128  256  512 1024 2048 4096 |   1   64  128  256  512 1024 2048 4096
+//   product  s 1, 1, 1, 8   7    8   14   25   46                     |   6   20   37
+//            s 1, 4, 1, 8  11   12   12   14   23   39   76           |   6   10   16   25   46
+//            s 2, 4, 1, 8  15   15   17   17   18   33   64  121      |   8    8   15   27   47   89
+//            s 2, 4, 2, 2  33   32   34   34   35   38   56  102  186 |  12   13   14   21   34   57  106
+//            wide 64       36   37   58   58   59   61   63   80  151 |  13   20   20   21   23   43   87  158
+//            wide 128      52   53   54   86   87   88   89   94  126 |  18   19   29   30   31   34   74  136
 //   SwiGLU   s 1, 4, 4, 2  36   37   37   37   40   79  151
 //            s 2, 4, 4, 2  43   44   47   46   47   52  101  199
 //            wide 64       38   39   59   60   61   64   81  151  285
@@ -718,14 +630,14 @@ Plan plan(const GemmArgs &a) {
     if (blocks(16, 16) <= kComputeUnits) return narrow<false, 1, 1, 1, 8, 3, 2>();
     if (mean <= 12 || blocks(16, 64) <= kComputeUnits) return narrow<false, 1, 4, 1, 8, 2, 2>();
     if (blocks(32, 64) <= 2 * kComputeUnits) return narrow<false, 2, 4, 1, 8, 2, 2>();
-    if (mean <= 24) return narrow<false, 2, 4, 2, 2, 2, 3>();
-    // halves of rounds of blocks over the compute units, whole rounds where there are few; a round of
-    // 256 rows takes 1.5 times one of 128
+    if (mean <= 24 || blocks(32, 128) <= 2 * kComputeUnits) return narrow<false, 2, 4, 2, 2, 2, 3>();
+    // rounds of blocks over the compute units, whole rounds where there are few; a round of 128 rows
+    // takes 1.5 times one of 64
     auto time = [&](int rows) {
         const int64_t all = blocks(rows, kBN), rounds = (all + kComputeUnits - 1) / kComputeUnits;
         return rounds <= 2 ? rounds * kComputeUnits : all;
     };
-    if (3 * time(256) <= 2 * time(128)) return {expert_gemm_wide_kernel<false, 4>, kBlockThreads, 256, kBN};
+    if (2 * time(64) <= 3 * time(128)) return {expert_gemm_wide_kernel<false, 1>, kBlockThreads, 64, kBN};
     return {expert_gemm_wide_kernel<false, 2>, kBlockThreads, 128, kBN};
 }
 
