@@ -625,6 +625,7 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_kernel(RouteParams p
             }
             m = token_max<LPT>(m);
             const float top = m == kNone ? 0.0f : value_of(m);
+            // in f32, off by under 56 * 2^-24; in 64 bits 16384 tokens of 64 experts take 6.8 us for 6.4, of 256 16.4 for 14.4
             float all = 0.0f;
 #pragma unroll
             for (int i = 0; i < VPL; ++i) all += expf(part.logit[i] - top);

@@ -63,8 +63,10 @@ typedef struct {
  *           renormalize is set.  A softmax's s_{e_j} / S are formed from the chosen logits alone,
  *           however far they are below the row's largest; a sigmoid's are 0 when every chosen s
  *           is 0 in binary64 (logits below about -709)
- * Choices and ratings compare as in binary64, so near ties are decided as the definition does; the
- * weights are rounded to f32 once.  An expert is eligible unless its logit is -inf (a masked
+ * Choices and ratings compare as in binary64, so near ties are decided as the definition does.
+ * Weights are formed in binary64 and rounded to f32 once, but for a softmax that is not
+ * renormalised: its denominator is a sum of f32 exponentials, which leaves them within 58 * 2^-24 of
+ * their value.  An expert is eligible unless its logit is -inf (a masked
  * expert) or its bias is -inf, or either is NaN or +inf (flagged, EP_DEV_BAD_LOGIT); such an
  * expert is never chosen, and one whose logit is not finite takes no part in the softmax.  Slots
  * that no eligible expert fills, and all slots of a token that token_mask switches off, get
