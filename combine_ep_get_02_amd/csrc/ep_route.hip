@@ -737,12 +737,7 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_backward_kernel(Rout
         part = scale * g * s;
         if (whole_row) {
             mean = token_sum<LPT>(part);
-            bool first = true;  // an expert named by several slots gets the mean's share once
-            for (int j = 0; j < p.K; ++j) {
-                const int e = LPT == kWave ? readlane32(id, j) : __shfl(id, base + j);
-                first = first && !(j < at && e == id);
-            }
-            if (first) part -= mean * s;
+            part -= mean * s;
         }
     }
     const float slot = (float)(part * rest);
@@ -753,17 +748,36 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_backward_kernel(Rout
         const int e0 = from + at * VPL;
         float d[VPL];
 #pragma unroll
-        for (int i = 0; i < VPL; ++i)  // experts without a slot have a gradient there too
-            d[i] = whole_row ? -(expf(logit[i] - top) / sum * share) : 0.0f;
-        uint32_t named = 0;
+        for (int i = 0; i < VPL; ++i) d[i] = 0.0f;
+        uint32_t named = 0, again = 0;  // elements in a slot, and in one more
         for (int j = 0; j < p.K; ++j) {
             const int e = (LPT == kWave ? readlane32(id, j) : __shfl(id, base + j)) - e0;
             const float v = LPT == kWave ? readlanef(slot, j) : __shfl(slot, base + j);
 #pragma unroll
+            for (int i = 0; i < VPL; ++i)
+                if (e == i) d[i] += v;
+            const uint32_t bit = (uint32_t)e < VPL ? 1u << e : 0u;
+            again |= named & bit;
+            named |= bit;
+        }
+        if (whole_row) {
+            // the mean's share: experts without a slot lose it here, of the others each slot has lost it
+            float lost[VPL];
+#pragma unroll
             for (int i = 0; i < VPL; ++i) {
-                if (e == i) {
-                    d[i] = (named >> i & 1u) != 0u ? d[i] + v : v;
-                    named |= 1u << i;
+                lost[i] = expf(logit[i] - top) / sum * share;
+                if ((named >> i & 1u) == 0u) d[i] = -lost[i];
+            }
+            if (ballot64(again != 0u) != 0ull) {  // and those in several slots get it back but for once
+                named = 0;
+                for (int j = 0; j < p.K; ++j) {
+                    const int e = __shfl(id, base + j) - e0;
+#pragma unroll
+                    for (int i = 0; i < VPL; ++i) {
+                        if (e != i) continue;
+                        if ((named >> i & 1u) != 0u) d[i] += lost[i];
+                        named |= 1u << i;
+                    }
                 }
             }
         }
