@@ -54,8 +54,8 @@ constexpr int kWaves = 4;
 
 // One wave per (token, segment of 64 16-byte units).  Up to kBatch rows' segments are loaded before
 // the first is used: a row at a time, a wave would wait out the memory's latency k times (prefill,
-// 4096 tokens of 8 rows of 7168: 88-93 us with 1 to 4 units a lane and batches of 2 to 8 alike, 5.7 to
-// 6.0 TB/s; 128 tokens: 8.8 us, 10 us a row at a time).
+// 4096 tokens of 8 rows of 7168: 87-93 us with 1 to 4 units a lane and batches of 2 to 8 alike, 5.7 to
+// 6.1 TB/s; 128 tokens: 4.9 us, a launch included).
 constexpr int kBatch = 8;
 __global__ __launch_bounds__(kWaves *kWave) void combine_grouped_kernel(Params p) {
     const int lane = threadIdx.x & (kWave - 1);
@@ -126,8 +126,8 @@ __device__ __forceinline__ void zero_padding(const Params &p) {
 // One block per token: the token's gradient row is scaled into each of its grouped rows, and its
 // product with that row's output summed over the block.  The gradient row stays in registers, UPT
 // 16-byte units a thread (rows of up to 64 WAVES UPT units; longer ones in turns), and the next row's
-// outputs are loaded while one is worked on.  Bound by HBM: 16384 tokens of 6 rows of 4096 take 329 us for 1.75
-// GB, 5.3 TB/s; 1000 tokens of 8 rows of 7168 with padding 49 us.
+// outputs are loaded while one is worked on.  Bound by HBM: 16384 tokens of 6 rows of 4096 take 327 us for 1.75
+// GB, 5.3 TB/s; 1000 tokens of 8 rows of 7168 with padding 48 us.
 template <int WAVES, int UPT>
 __global__ __launch_bounds__(WAVES *kWave) void combine_grouped_backward_kernel(Params p) {
     __shared__ float s_dot[kMaxTopk][WAVES];
@@ -221,8 +221,9 @@ hipError_t launch_combine_grouped_backward(const ep_shape_t &s, const CombineGro
     int64_t blocks = a.num_rows / 16 < 1024 ? a.num_rows / 16 + 1 : 1024;
     if (p.T > blocks) blocks = p.T;
     if (p.T == 0 && a.num_rows == 0) return hipSuccess;
-    // rows up to 4 KiB in one turn of four waves; wider ones take 8 waves of two units (16 KiB a turn):
-    // 4096-wide rows 292-300 us at 16384 tokens (5.3 TB/s), as 4 or 16 waves do
+    // rows up to 4 KiB in one turn of four waves; wider ones take 8 waves of two units (16 KiB a turn).  16384 tokens of
+    // 6 rows of 4096 / 1000 of 8 rows of 7168 with padding, us in a graph: 323 / 48; 4 waves of two units 330 / 51, of
+    // four 325 / 48, 16 waves of one 338 / 49
     if (p.units <= 4 * kWave) return start_kernel(combine_grouped_backward_kernel<4, 1>, blocks, 4 * kWave, stream, p);
     return start_kernel(combine_grouped_backward_kernel<8, 2>, blocks, 8 * kWave, stream, p);
 }

@@ -136,10 +136,11 @@ constexpr int kBN = 256;  // weight rows of a wide block
 // scaled into the wave's sums by one FMA each (a scale covers 128 channels).  The scaled sums have to be in
 // registers that vector instructions reach.
 //
-// Bound by the f16 matrix instructions, the conversions to f16 and the LDS reads that feed them: those three alone
-// reach 1.55 PFLOP/s on such data, the instructions alone 1.82.  SwiGLU of 32768 rows of 32 experts, 7168 channels
-// to 2048: 1920 us, 1.00 PFLOP/s; product of as many rows, 2048 channels to 7168: 1040 us, 0.93.  (The E4M3
-// instructions took the product in 606 us, without the sums' last bits.)
+// SwiGLU of 32768 rows of 32 experts, 7168 channels to 2048: 1875 us (median of 20; 1816 the least), 1.03 PFLOP/s;
+// product of as many rows, 2048 channels to 7168: 996 us (963), 0.97.  Matrix instructions are at work in 48 to 51% of
+// a SIMD's cycles and the other vector instructions (conversions, scaling) issue in 45 to 48%: the two waves of a SIMD
+// leave the barrier together and convert together, so the two kinds hardly overlap.  LDS is in use for 15%, and the
+// clock is at 1.95 of 2.4 GHz.  (The E4M3 instructions took the product in 606 us, without the sums' last bits.)
 template <bool SWIGLU, int MI>
 __global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(GemmArgs p, int col_tiles) {
     constexpr int WM = 2, WN = 4, BM = 32 * MI * WM, HALF = 32;
@@ -369,12 +370,12 @@ __global__ __launch_bounds__(kBlockThreads, 2) void expert_gemm_wide_kernel(Gemm
 // barriers: a wave has loads under way while it multiplies.  The KS waves of a group take every KS-th
 // block of channels and add up through LDS at the end.
 //
-// With rows for many experts this is bound by the weights' bytes: 128 rows of 32 experts take 168 us
-// for 0.94 GB (SwiGLU, 7168 channels to 2048) and 81 us for 0.47 GB (product, 2048 to 7168), 5.5 and
-// 5.8 TB/s.  A few blocks alone are bound by what one compute unit takes in: 16 bytes a clock where
+// With rows for many experts this is bound by the weights' bytes: 128 rows of 32 experts take 162 us
+// for 0.94 GB (SwiGLU, 7168 channels to 2048) and 77 us for 0.47 GB (product, 2048 to 7168), 5.8 and
+// 6.1 TB/s.  A few blocks alone are bound by what one compute unit takes in: 16 bytes a clock where
 // neighbouring lanes read different rows, as the matrix instructions want them, and over 30 where eight
 // lanes read a row's 128 bytes.  So they do that, and the wave turns its tile round in LDS that no other
-// wave touches (16 rows of one expert, 2048 of 7168 channels: 23 -> 13 us; the SwiGLU above 180 -> 168).
+// wave touches (16 rows of one expert, 2048 of 7168 channels: 23 -> 12 us; the SwiGLU above 180 -> 162).
 template <bool SWIGLU, int MF, int WF, int NG, int KS, int DEEP, int WAVES>
 __global__ __launch_bounds__(NG *KS *kWave, WAVES) void expert_gemm_narrow_kernel(GemmArgs p, int col_tiles) {
     static_assert(!SWIGLU || 8 * WF * NG == 128, "a block holds a scale's 128 outputs");

@@ -54,7 +54,7 @@ struct GemmArgs {
     int32_t *dev_status;
     bool swiglu;
 };
-// False when the launch would need more than 2^31 - 1 blocks.
+// False when the launch would need more than 2^31 - 1 threads.
 bool gemm_grid_ok(const GemmArgs &a);
 hipError_t launch_expert_gemm(const GemmArgs &a, hipStream_t stream);
 

@@ -22,12 +22,12 @@ namespace {
 constexpr int kRouteWaves = 4;  // waves per block
 // From this many tokens on they share waves.  Few tokens are bound by the latency of one wave's steps, which
 // more experts a lane lengthen; many by the vector instructions of all.  8 slots, router (softmax) / its
-// gradient with 64, 32 and 16 lanes, us:
+// gradient (softmax, not renormalised) with 64, 32 and 16 lanes, us:
 //   tokens                    2048                          4096                          16384
-//   64 experts                4.6/4.2  4.6/4.3  4.8/4.6     5.5/5.4  4.9/4.6  4.8/4.7     13.0/13.4  9.2/8.7  6.5/6.9
-//   128 experts               4.8/4.6  4.9/4.8  5.5/5.5     6.0/6.2  5.4/5.3  5.6/5.8     14.5/14.7  10.4/11.1  8.0/9.2
-//   256 experts in 8 groups   7.9/5.3  9.1/6.0  17.7/-      11/7.3   10/6.8   18/-        29/18.6    25/15.3    30/-
-// (512 experts in 8 groups, 16384 tokens, 64 and 32 lanes: 40/30 and 41/30.)
+//   64 experts                4.6/3.5  4.6/3.7  4.8/4.0     5.5/4.5  4.9/4.0  4.8/4.1     13.0/10.6  9.2/7.7  6.5/6.3
+//   128 experts               4.8/4.0  4.9/4.1  5.5/4.8     6.0/5.4  5.4/4.5  5.6/5.2     14.5/13.6  10.4/9.9  8.0/9.1
+//   256 experts in 8 groups   7.9/4.6  9.1/5.1  17.7/8.1    11/6.4   10/5.9   18/8.7      29/18.4    25/15.4   30/17.3
+// (512 experts in 8 groups, 16384 tokens, router with 64 and 32 lanes: 40 and 41.)
 constexpr int64_t kManyTokens = 4096;
 
 struct RouteParams {
@@ -562,7 +562,9 @@ __device__ __forceinline__ void choose(const RouteParams &p, const Part<VPL> &t,
 
 // One launch routes a token per LPT lanes.  128 tokens of 256 experts in 8 groups take 7.3 us on the card, a
 // launch (about 3) included: latency, of loads, group ratings and a chain of cross-lane steps a slot.  16384
-// tokens of 64 experts take 6 us, over the 0.6 that their bytes need, for the same reason.
+// tokens of 64 experts take 6 us, over the 0.6 that their bytes need, for the same reason.  Many tokens of many experts
+// are bound by the selection, which looks through all of a lane's keys a round: 7747 tokens of 471 experts with a bias
+// take 11.7 us for one slot and 17.5 for eight, 0.8 to 0.9 a slot.
 template <int LPT, int VPL, bool BF16>
 __global__ __launch_bounds__(kRouteWaves *kWave) void route_kernel(RouteParams p) {
     constexpr int kTokens = kWave / LPT;  // of a wave
@@ -645,9 +647,9 @@ __global__ __launch_bounds__(kRouteWaves *kWave) void route_kernel(RouteParams p
     }
 }
 
-// VPL experts a lane at a time, all of a token's at once where they fit.  4096 tokens of 256 experts take 6.8 us on
-// the card (8.8 MB, 1.7 us of bytes), 16384 tokens of 64 in bf16 6.3 us: a launch and the latency of one wave's
-// loads, sums over its slots and stores.
+// VPL experts a lane at a time, all of a token's at once where they fit.  4096 tokens of 256 experts take 5.7 us on
+// the card (sigmoid, renormalised; 8.8 MB, 1.7 us of bytes), 16384 tokens of 64 in bf16 6.7 us (softmax, not
+// renormalised): a launch and the latency of one wave's loads, sums over its slots and stores.
 template <int LPT, int VPL, bool BF16>
 __global__ __launch_bounds__(kRouteWaves *kWave) void route_backward_kernel(RouteBackwardParams p) {
     constexpr int kTokens = kWave / LPT, kSpan = LPT * VPL;
